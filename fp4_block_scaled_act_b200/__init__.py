@@ -12,6 +12,7 @@ allocate outputs and workspaces with torch and call the same entry points.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from dataclasses import dataclass
@@ -22,6 +23,12 @@ from ._build import build
 
 MXFP4, NVFP4 = 0, 1
 _FMT = {"mxfp4": MXFP4, "nvfp4": NVFP4, MXFP4: MXFP4, NVFP4: NVFP4}
+
+NORM_NONE, NORM_HEAD, NORM_TOKEN = 0, 1, 2
+_NORM = {None: NORM_NONE, "none": NORM_NONE, "head": NORM_HEAD, "token": NORM_TOKEN, NORM_NONE: NORM_NONE,
+         NORM_HEAD: NORM_HEAD, NORM_TOKEN: NORM_TOKEN}
+ROPE_INTERLEAVED, ROPE_HALF = 0, 1
+_ROPE = {"interleaved": ROPE_INTERLEAVED, "half": ROPE_HALF, ROPE_INTERLEAVED: ROPE_INTERLEAVED, ROPE_HALF: ROPE_HALF}
 
 STATUS = ["FP4_OK", "FP4_ERR_INVALID_ARG", "FP4_ERR_UNSUPPORTED_SHAPE", "FP4_ERR_MISALIGNED",
           "FP4_ERR_WORKSPACE", "FP4_ERR_ARCH", "FP4_ERR_CUDA", "FP4_ERR_TIMEOUT"]
@@ -39,6 +46,7 @@ EXPORTS = [
     "fp4_attn_pv",
     "fp4_attn_fused",
     "fp4_attn_fused_trace",
+    "fp4_rope_table", "fp4_qk_norm_rope", "fp4_qk_norm_rope_quantize_heads", "fp4_dequantize_heads",
 ]
 
 
@@ -60,6 +68,7 @@ def lib():
             raise RuntimeError(f"{_LIB_PATH} is missing: run fp4_block_scaled_act_b200.build() first")
         L = ctypes.CDLL(_LIB_PATH)
         P, I64, I, SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
+        D, F = ctypes.c_double, ctypes.c_float
         sig = {
             "fp4_codes_bytes": (SZ, [I, I64, I64]),
             "fp4_sf_bytes": (SZ, [I, I64, I64]),
@@ -95,6 +104,11 @@ def lib():
                                    P]),
             "fp4_attn_fused_trace": (I, [I, P, P, I64, P, P, I64, P, P, I64, I64, I64, ctypes.c_float, P, P, P, P, P,
                                          P, I64, P, P, P, P]),
+            "fp4_rope_table": (I, [P, I64, I, P, D, D, I64, F, P, P]),
+            "fp4_qk_norm_rope": (I, [P, I64, I64, P, I64, I64, I64, I64, I, P, P, F, P, I64, I, P, I64, P, I64, P]),
+            "fp4_qk_norm_rope_quantize_heads": (I, [I, P, I64, I64, P, I64, I64, I64, I64, I, P, P, F, P, I64, I, P, P,
+                                                    P, P, P, P, P]),
+            "fp4_dequantize_heads": (I, [I, P, P, I64, I64, I64, P, P, I64, P]),
             "fp4_sync_status": (I, [P]),
             "fp4_status_string": (ctypes.c_char_p, [I]),
             "fp4_set_wait_timeout_ns": (None, [ctypes.c_uint64]),
@@ -123,6 +137,15 @@ def _ptr(t) -> Optional[int]:
         raise ValueError("expected a CUDA tensor")
     if not t.is_contiguous():
         raise ValueError("expected a contiguous tensor")
+    return t.data_ptr()
+
+
+def _rows_ptr(t) -> Optional[int]:
+    """Pointer of a [T, H, D] tensor whose rows may lie apart (the caller passes its row stride)."""
+    if t is None or isinstance(t, int):
+        return t
+    if not t.is_cuda:
+        raise ValueError("expected a CUDA tensor")
     return t.data_ptr()
 
 
@@ -318,6 +341,40 @@ def fp4_attn_fused_trace(fmt, q_codes, q_sf, T_q: int, k_codes, k_sf, T_kv: int,
                                       _ptr(vt_codes), _ptr(vt_sf), H, D, head, scale, _ptr(g_q), _ptr(g_k),
                                       _ptr(g_v), _ptr(p_global), _ptr(stats), _ptr(o), trace_tile, _ptr(trace_m),
                                       _ptr(trace_codes), _ptr(trace_sf), _stream(stream)), "fp4_attn_fused_trace")
+
+
+def fp4_rope_table(positions, T: int, axes: int, axis_dims, theta: float, factor: float, window: int,
+                   amplitude: float, table, stream=None):
+    dims = (ctypes.c_int64 * len(axis_dims))(*axis_dims)
+    _check(lib().fp4_rope_table(_ptr(positions), T, axes, dims, theta, factor, window, amplitude, _ptr(table),
+                                _stream(stream)), "fp4_rope_table")
+
+
+def fp4_qk_norm_rope(q, q_stride: int, H_q: int, k, k_stride: int, H_k: int, T: int, D: int, norm, q_weight, k_weight,
+                     eps: float, table, rot: int, layout, q_out, q_out_stride: int, k_out, k_out_stride: int,
+                     stream=None):
+    """q, k, q_out and k_out may be rows of a larger buffer (strides in elements)."""
+    _check(lib().fp4_qk_norm_rope(_rows_ptr(q), q_stride, H_q, _rows_ptr(k), k_stride, H_k, T, D, _NORM[norm],
+                                  _ptr(q_weight), _ptr(k_weight), eps, _ptr(table), rot, _ROPE[layout],
+                                  _rows_ptr(q_out), q_out_stride, _rows_ptr(k_out), k_out_stride, _stream(stream)),
+           "fp4_qk_norm_rope")
+
+
+def fp4_qk_norm_rope_quantize_heads(fmt, q, q_stride: int, H_q: int, k, k_stride: int, H_k: int, T: int, D: int, norm,
+                                    q_weight, k_weight, eps: float, table, rot: int, layout, g_q, g_k, q_codes, q_sf,
+                                    k_codes, k_sf, stream=None):
+    """q and k may be rows of a larger buffer (strides in elements)."""
+    _check(lib().fp4_qk_norm_rope_quantize_heads(_fmt(fmt), _rows_ptr(q), q_stride, H_q, _rows_ptr(k), k_stride, H_k,
+                                                 T, D, _NORM[norm], _ptr(q_weight), _ptr(k_weight), eps, _ptr(table),
+                                                 rot, _ROPE[layout], _ptr(g_q), _ptr(g_k), _ptr(q_codes), _ptr(q_sf),
+                                                 _ptr(k_codes), _ptr(k_sf), _stream(stream)),
+           "fp4_qk_norm_rope_quantize_heads")
+
+
+def fp4_dequantize_heads(fmt, codes, sf, T: int, H: int, D: int, g, x, x_stride: int, stream=None):
+    """x may be rows of a larger buffer (x_stride in elements)."""
+    _check(lib().fp4_dequantize_heads(_fmt(fmt), _ptr(codes), _ptr(sf), T, H, D, _ptr(g), _rows_ptr(x), x_stride,
+                                      _stream(stream)), "fp4_dequantize_heads")
 
 
 def fp4_sync_status(stream=None) -> int:
@@ -574,6 +631,146 @@ def linear_gelu_quant(x, pw: PackedWeight, bias=None, a_global=None, h_global=No
     fp4_linear_gelu_quant(pw.fmt, x, M, K, N, pw.codes, pw.sf, pw.w_global, a_global, bias, h_global, codes, sf,
                           workspace, workspace.numel(), stream)
     return codes, sf
+
+
+# ----------------------------------------------------------------------------- around the attention
+# These helpers check types, shapes and devices, since the C calls see only addresses.
+def _expect(t, what: str, dtype, device, shape=None):
+    """t is a contiguous CUDA tensor of this type on this device (and of this shape), or None."""
+    if t is None:
+        return
+    if t.dtype != dtype or t.device != device:
+        raise ValueError(f"{what}: expected {dtype} on {device}, got {t.dtype} on {t.device}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{what}: expected a contiguous tensor")
+
+
+def _expect_rows(t, what: str, device=None):
+    """t is a bf16 CUDA tensor [T, H, D] with contiguous heads; returns its row stride in elements."""
+    import torch
+
+    if t.dim() != 3 or t.dtype != torch.bfloat16 or not t.is_cuda:
+        raise ValueError(f"{what}: expected a bf16 CUDA tensor [T, H, D], got {t.dtype} {tuple(t.shape)} on {t.device}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{what}: expected a tensor on {device}, got {t.device}")
+    T, H, D = t.shape
+    if t.stride(2) != 1 or (H > 1 and t.stride(1) != D):
+        raise ValueError(f"{what}: heads must be contiguous (strides {t.stride()})")
+    return t.stride(0) if T > 1 else H * D
+
+
+def _on(device):
+    """Context in which the launches go to the tensors' device."""
+    import torch
+
+    return contextlib.nullcontext() if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+
+
+def rope_table(positions, axis_dims, theta: float = 10000.0, factor: float = 1.0, window: int = 0,
+               amplitude: float = 1.0, table=None, stream=None):
+    """Rotary table of int32 positions [T, axes] (CUDA): fp32 [T, sum(axis_dims)] (cos, sin) pairs."""
+    import torch
+
+    if positions.dim() != 2 or positions.shape[1] != len(axis_dims):
+        raise ValueError(f"positions: expected [T, {len(axis_dims)}], got {tuple(positions.shape)}")
+    _expect(positions, "positions", torch.int32, positions.device)
+    T, axes = positions.shape
+    if table is None:
+        table = torch.empty((T, sum(axis_dims)), dtype=torch.float32, device=positions.device)
+    else:
+        _expect(table, "table", torch.float32, positions.device, (T, sum(axis_dims)))
+    with _on(positions.device):
+        fp4_rope_table(positions, T, axes, axis_dims, theta, factor, window, amplitude, table, stream)
+    return table
+
+
+def _norm_rope_args(q, k, norm, q_weight, k_weight, table):
+    import torch
+
+    q_stride = _expect_rows(q, "q")
+    T, H_q, D = q.shape
+    k_stride, H_k = 0, 0
+    if k is not None:
+        k_stride, H_k = _expect_rows(k, "k", q.device), k.shape[1]
+        if k.shape[0] != T or k.shape[2] != D:
+            raise ValueError(f"k: expected [{T}, heads, {D}], got {tuple(k.shape)}")
+    token = _NORM[norm] == NORM_TOKEN
+    _expect(q_weight, "q_weight", torch.float32, q.device, (H_q * D if token else D,))
+    _expect(k_weight, "k_weight", torch.float32, q.device, (H_k * D if token else D,))
+    rot = 0
+    if table is not None:
+        rot = table.shape[-1]
+        _expect(table, "table", torch.float32, q.device, (T, rot))
+    return q_stride, H_q, k_stride, H_k, T, D, rot
+
+
+def qk_norm_rope(q, k=None, norm="head", q_weight=None, k_weight=None, eps: float = 1e-6, table=None,
+                 layout="interleaved", q_out=None, k_out=None, stream=None):
+    """RMS norm ("head", "token" or "none") and rotation of bf16 queries [T, H_q, D] and, if given, keys
+    [T, H_k, D] in one launch; rows may be slices of a fused projection.  table: fp32 [T, rot] from
+    rope_table, or None.  Returns (q_out, k_out), or q_out alone; q_out = q rotates in place."""
+    import torch
+
+    q_stride, H_q, k_stride, H_k, T, D, rot = _norm_rope_args(q, k, norm, q_weight, k_weight, table)
+    if q_out is None:
+        q_out = torch.empty((T, H_q, D), dtype=torch.bfloat16, device=q.device)
+    if k is not None and k_out is None:
+        k_out = torch.empty((T, H_k, D), dtype=torch.bfloat16, device=q.device)
+    strides = []
+    for out, x, what in ((q_out, q, "q_out"), (k_out, k, "k_out")):
+        strides.append(_expect_rows(out, what, q.device) if out is not None else 0)
+        if out is not None and (x is None or out.shape != x.shape):
+            raise ValueError(f"{what}: expected the shape of its input, got {tuple(out.shape)}")
+    with _on(q.device):
+        fp4_qk_norm_rope(q, q_stride, H_q, k, k_stride, H_k, T, D, norm, q_weight, k_weight, eps, table, rot, layout,
+                         q_out, strides[0], k_out, strides[1], stream)
+    return q_out if k is None else (q_out, k_out)
+
+
+def qk_norm_rope_quantize_heads(q, k=None, fmt="mxfp4", norm="head", q_weight=None, k_weight=None, eps: float = 1e-6,
+                                table=None, layout="interleaved", g_q=None, g_k=None, stream=None):
+    """qk_norm_rope's result as head-major FP4 (codes, scales), as quantize_heads makes them of it:
+    ((q_codes, q_sf), (k_codes, k_sf)), or the queries' pair alone.  NVFP4: g_q, g_k device globals."""
+    import torch
+
+    f = _fmt(fmt)
+    q_stride, H_q, k_stride, H_k, T, D, rot = _norm_rope_args(q, k, norm, q_weight, k_weight, table)
+    _expect(g_q, "g_q", torch.float32, q.device)
+    _expect(g_k, "g_k", torch.float32, q.device)
+    Tpad = (T + 127) // 128 * 128
+    outs = []
+    for H in (H_q, H_k) if k is not None else (H_q,):
+        outs.append((torch.empty((H, Tpad, D // 2), dtype=torch.uint8, device=q.device),
+                     torch.empty((H, fp4_heads_sf_bytes(f, T, H, D) // H), dtype=torch.uint8, device=q.device)))
+    kc, ks = outs[1] if k is not None else (None, None)
+    with _on(q.device):
+        fp4_qk_norm_rope_quantize_heads(f, q, q_stride, H_q, k, k_stride, H_k, T, D, norm, q_weight, k_weight, eps,
+                                        table, rot, layout, g_q, g_k, outs[0][0], outs[0][1], kc, ks, stream)
+    return outs[0] if k is None else tuple(outs)
+
+
+def dequantize_heads(heads, T: int, fmt="mxfp4", g=None, x=None, stream=None):
+    """quantize_heads' (codes, scales) of T tokens back to bf16 [T, H, 128]."""
+    import torch
+
+    f = _fmt(fmt)
+    codes, sf = heads
+    H, Tpad, half_d = codes.shape
+    if Tpad != (T + 127) // 128 * 128:
+        raise ValueError(f"codes of {Tpad} padded tokens do not belong to {T} tokens")
+    _expect(codes, "codes", torch.uint8, codes.device)
+    _expect(sf, "scales", torch.uint8, codes.device, (H, fp4_heads_sf_bytes(f, T, H, 2 * half_d) // H))
+    _expect(g, "g", torch.float32, codes.device)
+    if x is None:
+        x = torch.empty((T, H, 2 * half_d), dtype=torch.bfloat16, device=codes.device)
+    stride = _expect_rows(x, "x", codes.device)
+    if tuple(x.shape) != (T, H, 2 * half_d):
+        raise ValueError(f"x: expected [{T}, {H}, {2 * half_d}], got {tuple(x.shape)}")
+    with _on(codes.device):
+        fp4_dequantize_heads(f, codes, sf, T, H, 2 * half_d, g, x, stride, stream)
+    return x
 
 
 class HostPipeline:

@@ -5,12 +5,14 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 #include <mutex>
 
 #include "fp4bsa.h"
 #include "attn.cuh"
 #include "attn_fused.cuh"
 #include "gemm.cuh"
+#include "norm_rope.cuh"
 #include "quant.cuh"
 
 using namespace fp4;
@@ -1029,6 +1031,191 @@ fp4_status_t w4a4_svd_linear(const void* x_bf16, int64_t M, int64_t K, int64_t N
     float* partial = lr_partial_bytes(M, K) ? reinterpret_cast<float*>(u + align256((size_t)M * rank * 4)) : nullptr;
     if ((s = w4a4_quantize_impl(x_bf16, M, K, l1_bf16, rank, xc, xs, u, partial, stream)) != FP4_OK) return s;
     return w4a4_gemm(xc, xs, u, M, K, N, r_codes, r_sf, l2_bf16, rank, bias_f16, y_bf16, stream);
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------------------
+// Rotary tables, the norm and rotation of queries and keys, decoded heads
+namespace {
+inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Persistent launch: a resident wave of blocks at most.
+template <bool TOKEN, int OUT, bool HALF, int D>
+fp4_status_t launch_norm_rope(const DeviceState* ds, const NormRopeParams& p, int tensors, cudaStream_t st) {
+    const auto kernel = norm_rope_kernel<TOKEN, OUT, HALF, D>;
+    const int H = std::max(p.t[0].H, tensors > 1 ? p.t[1].H : 0);
+    const int64_t rows = OUT == NR_BF16 ? p.T : (p.T + 127) / 128 * 128;
+    const int threads = TOKEN ? (H * (D / 16) + 31) / 32 * 32 : 256;
+    const int64_t need = TOKEN ? rows : (rows * H * (D / 16) + 255) / 256;
+    int occ = 0;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, kernel, threads, 0) != cudaSuccess || occ < 1)
+        return FP4_ERR_CUDA;
+    const int64_t blocks = std::min<int64_t>(need, (int64_t)ds->sm_count * occ);
+    kernel<<<dim3((unsigned)blocks, (unsigned)tensors), threads, 0, st>>>(p);
+    return launched();
+}
+
+template <int OUT, int D>
+fp4_status_t pick_norm_rope(const DeviceState* ds, const NormRopeParams& p, int tensors, bool half, cudaStream_t st) {
+    if (p.norm == NORM_TOKEN)
+        return half ? launch_norm_rope<true, OUT, true, D>(ds, p, tensors, st)
+                    : launch_norm_rope<true, OUT, false, D>(ds, p, tensors, st);
+    return half ? launch_norm_rope<false, OUT, true, D>(ds, p, tensors, st)
+                : launch_norm_rope<false, OUT, false, D>(ds, p, tensors, st);
+}
+
+// The arguments that both forms share; p.t[] holds the tensors' own.
+fp4_status_t check_norm_rope(const NormRopeParams& p, int tensors, int64_t H_q, int64_t H_k, int64_t D,
+                             fp4_norm_t norm, float eps, fp4_rope_layout_t layout, int rot_unit) {
+    if (norm != FP4_NORM_NONE && norm != FP4_NORM_HEAD && norm != FP4_NORM_TOKEN) return FP4_ERR_INVALID_ARG;
+    if (layout != FP4_ROPE_INTERLEAVED && layout != FP4_ROPE_HALF) return FP4_ERR_INVALID_ARG;
+    if (p.T < 1 || !(eps >= 0.0f) || !(eps < 3.0e38f)) return FP4_ERR_INVALID_ARG;
+    if (p.rot < 0 || (p.rot > 0) != (p.table != nullptr)) return FP4_ERR_INVALID_ARG;
+    if (D != 64 && D != 128) return FP4_ERR_UNSUPPORTED_SHAPE;
+    if (p.rot > D || p.rot % rot_unit != 0) return FP4_ERR_UNSUPPORTED_SHAPE;
+    if (!aligned16(p.table)) return FP4_ERR_MISALIGNED;
+    for (int i = 0; i < tensors; ++i) {
+        const NormRopeTensor& t = p.t[i];
+        const int64_t H = i ? H_k : H_q;
+        if (!t.x || H < 1) return FP4_ERR_INVALID_ARG;
+        if (norm == FP4_NORM_NONE && t.weight) return FP4_ERR_INVALID_ARG;
+        // the token norm keeps a token in one block, 16 values a thread; units are numbered with 32 bits
+        if (H > 16384 / D && norm == FP4_NORM_TOKEN) return FP4_ERR_UNSUPPORTED_SHAPE;
+        if (H >= kMaxDim / D || p.T >= kMaxDim || (p.T + 127) / 128 * 128 * H * (D / 16) >= ((int64_t)1 << 31))
+            return FP4_ERR_UNSUPPORTED_SHAPE;
+        if (t.stride < H * D) return FP4_ERR_INVALID_ARG;
+        if (!aligned16(t.x) || (t.stride & 7) || !aligned16(t.weight)) return FP4_ERR_MISALIGNED;
+    }
+    return FP4_OK;
+}
+}  // namespace
+
+extern "C" {
+
+fp4_status_t fp4_rope_table(const int32_t* positions, int64_t T, int axes, const int64_t* axis_dims, double theta,
+                            double factor, int64_t window, float amplitude, float* table, void* stream) {
+    if (!positions || !axis_dims || !table || T < 1 || axes < 1 || axes > 4) return FP4_ERR_INVALID_ARG;
+    if (!(theta > 1.0) || !(theta < 1.0e30) || !(factor >= 1.0) || !(factor < 1.0e30) || window < 0 ||
+        !(amplitude > 0.0f) || !(amplitude < 3.0e38f))
+        return FP4_ERR_INVALID_ARG;
+    if (T >= kMaxDim) return FP4_ERR_UNSUPPORTED_SHAPE;
+    if (!aligned4(positions) || !aligned16(table)) return FP4_ERR_MISALIGNED;
+    RopeFreqs f{};
+    int64_t pairs = 0;
+    const double two_pi = 6.283185307179586476925287;
+    for (int a = 0; a < axes; ++a) {
+        const int64_t d = axis_dims[a];
+        if (d < 0 || (d & 1) || pairs + d / 2 > ROPE_MAX_PAIRS) return FP4_ERR_UNSUPPORTED_SHAPE;
+        // by parts: pair j turns window / wavelength_j times within the trained window; 32 turns and
+        // more keep their frequency, one turn and fewer are slowed by the factor, a ramp lies between
+        const auto pair_of = [&](double turns) {
+            return (double)d * std::log((double)window / (two_pi * turns)) / (2.0 * std::log(theta));
+        };
+        double lo = 0.0, hi = 0.0;
+        if (window > 0) {
+            lo = std::max(std::floor(pair_of(32.0)), 0.0);
+            hi = std::min(std::ceil(pair_of(1.0)), (double)(d - 1));
+        }
+        for (int64_t j = 0; j < d / 2; ++j) {
+            double w = std::pow(theta, -2.0 * (double)j / (double)d);
+            if (factor != 1.0) {
+                const double ramp =
+                    window > 0 ? std::min(std::max(((double)j - lo) / std::max(hi - lo, 1e-3), 0.0), 1.0) : 1.0;
+                w = w * (1.0 - ramp) + w / factor * ramp;
+            }
+            f.turns[pairs] = w / two_pi;
+            f.axis[pairs++] = (int8_t)a;
+        }
+    }
+    if (pairs < 1) return FP4_ERR_UNSUPPORTED_SHAPE;
+    DeviceState* ds;
+    fp4_status_t s = device_state(&ds);
+    if (s != FP4_OK) return s;
+    const int64_t blocks = std::min<int64_t>((T * pairs + 255) / 256, (int64_t)ds->sm_count * 8);
+    rope_table_kernel<<<(unsigned)blocks, 256, 0, static_cast<cudaStream_t>(stream)>>>(
+        positions, T, axes, (int)pairs, amplitude, f, reinterpret_cast<float2*>(table));
+    return launched();
+}
+
+fp4_status_t fp4_qk_norm_rope(const void* q_bf16, int64_t q_stride, int64_t H_q, const void* k_bf16, int64_t k_stride,
+                              int64_t H_k, int64_t T, int64_t D, fp4_norm_t norm, const float* q_weight,
+                              const float* k_weight, float eps, const float* table, int64_t rot,
+                              fp4_rope_layout_t layout, void* q_out, int64_t q_out_stride, void* k_out,
+                              int64_t k_out_stride, void* stream) {
+    if (!q_bf16 || !q_out || (k_bf16 != nullptr) != (k_out != nullptr)) return FP4_ERR_INVALID_ARG;
+    if (rot < 0 || rot > 1024) return FP4_ERR_UNSUPPORTED_SHAPE;
+    NormRopeParams p{};
+    p.T = T, p.norm = (int)norm, p.eps = eps, p.table = table, p.rot = (int)rot;
+    const int tensors = k_bf16 ? 2 : 1;
+    p.t[0] = {static_cast<const __nv_bfloat16*>(q_bf16), q_stride, (int)H_q, q_weight,
+              static_cast<__nv_bfloat16*>(q_out), q_out_stride, nullptr, nullptr, nullptr};
+    p.t[1] = {static_cast<const __nv_bfloat16*>(k_bf16), k_stride, (int)H_k, k_weight,
+              static_cast<__nv_bfloat16*>(k_out), k_out_stride, nullptr, nullptr, nullptr};
+    fp4_status_t s = check_norm_rope(p, tensors, H_q, H_k, D, norm, eps, layout, 16);
+    if (s != FP4_OK) return s;
+    for (int i = 0; i < tensors; ++i) {
+        if (p.t[i].out_stride < p.t[i].H * D) return FP4_ERR_INVALID_ARG;
+        if (!aligned16(p.t[i].out) || (p.t[i].out_stride & 7)) return FP4_ERR_MISALIGNED;
+    }
+    DeviceState* ds;
+    if ((s = device_state(&ds)) != FP4_OK) return s;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const bool half = layout == FP4_ROPE_HALF;
+    return D == 128 ? pick_norm_rope<NR_BF16, 128>(ds, p, tensors, half, st)
+                    : pick_norm_rope<NR_BF16, 64>(ds, p, tensors, half, st);
+}
+
+fp4_status_t fp4_qk_norm_rope_quantize_heads(fp4_fmt_t fmt, const void* q_bf16, int64_t q_stride, int64_t H_q,
+                                             const void* k_bf16, int64_t k_stride, int64_t H_k, int64_t T, int64_t D,
+                                             fp4_norm_t norm, const float* q_weight, const float* k_weight, float eps,
+                                             const float* table, int64_t rot, fp4_rope_layout_t layout,
+                                             const float* g_q, const float* g_k, uint8_t* q_codes, uint8_t* q_sf,
+                                             uint8_t* k_codes, uint8_t* k_sf, void* stream) {
+    if (!fmt_ok(fmt) || !q_bf16 || !q_codes || !q_sf) return FP4_ERR_INVALID_ARG;
+    if ((k_bf16 != nullptr) != (k_codes != nullptr) || (k_bf16 != nullptr) != (k_sf != nullptr))
+        return FP4_ERR_INVALID_ARG;
+    const bool nv = fmt == FP4_FMT_NVFP4;
+    if (nv != (g_q != nullptr) || (nv && k_bf16) != (g_k != nullptr)) return FP4_ERR_INVALID_ARG;
+    if (D != FP4_HEAD_DIM || rot < 0 || rot > 1024) return FP4_ERR_UNSUPPORTED_SHAPE;
+    NormRopeParams p{};
+    p.T = T, p.norm = (int)norm, p.eps = eps, p.table = table, p.rot = (int)rot;
+    const int tensors = k_bf16 ? 2 : 1;
+    p.t[0] = {static_cast<const __nv_bfloat16*>(q_bf16), q_stride, (int)H_q, q_weight, nullptr, 0, q_codes, q_sf, g_q};
+    p.t[1] = {static_cast<const __nv_bfloat16*>(k_bf16), k_stride, (int)H_k, k_weight, nullptr, 0, k_codes, k_sf, g_k};
+    // in the half layout a block of values lies in neighbouring lanes for rot = 0, 64 and 128
+    fp4_status_t s = check_norm_rope(p, tensors, H_q, H_k, D, norm, eps, layout, layout == FP4_ROPE_HALF ? 64 : 16);
+    if (s != FP4_OK) return s;
+    for (int i = 0; i < tensors; ++i)
+        if (!aligned16(p.t[i].codes) || !aligned16(p.t[i].sf) || !aligned4(p.t[i].g)) return FP4_ERR_MISALIGNED;
+    DeviceState* ds;
+    if ((s = device_state(&ds)) != FP4_OK) return s;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const bool half = layout == FP4_ROPE_HALF;
+    return nv ? pick_norm_rope<NR_NVFP4, 128>(ds, p, tensors, half, st)
+              : pick_norm_rope<NR_MXFP4, 128>(ds, p, tensors, half, st);
+}
+
+fp4_status_t fp4_dequantize_heads(fp4_fmt_t fmt, const uint8_t* codes, const uint8_t* sf, int64_t T, int64_t H,
+                                  int64_t D, const float* g, void* x_bf16, int64_t x_stride, void* stream) {
+    if (!fmt_ok(fmt) || !codes || !sf || !x_bf16 || T < 1 || H < 1) return FP4_ERR_INVALID_ARG;
+    if ((fmt == FP4_FMT_NVFP4) != (g != nullptr)) return FP4_ERR_INVALID_ARG;
+    if (D != FP4_HEAD_DIM || H >= kMaxDim / D || T >= kMaxDim || T * H * 8 >= ((int64_t)1 << 31))
+        return FP4_ERR_UNSUPPORTED_SHAPE;
+    if (x_stride < H * D) return FP4_ERR_INVALID_ARG;
+    if (!aligned16(codes) || !aligned16(sf) || !aligned16(x_bf16) || (x_stride & 7) || !aligned4(g))
+        return FP4_ERR_MISALIGNED;
+    DeviceState* ds;
+    fp4_status_t s = device_state(&ds);
+    if (s != FP4_OK) return s;
+    const int64_t blocks = std::min<int64_t>((T * H * 8 + 255) / 256, (int64_t)ds->sm_count * 8);
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const auto out = static_cast<__nv_bfloat16*>(x_bf16);
+    if (fmt == FP4_FMT_NVFP4)
+        dequant_heads_kernel<true><<<(unsigned)blocks, 256, 0, st>>>(codes, sf, T, (int)H, g, out, x_stride);
+    else
+        dequant_heads_kernel<false><<<(unsigned)blocks, 256, 0, st>>>(codes, sf, T, (int)H, g, out, x_stride);
+    return launched();
 }
 
 fp4_status_t fp4_sync_status(void* stream) {

@@ -460,6 +460,80 @@ fp4_status_t fp4_attn_fused_trace(fp4_fmt_t fmt, const uint8_t* q_codes, const u
                                   void* stats, void* o_bf16, int64_t trace_tile, float* trace_m,
                                   uint8_t* trace_codes, uint8_t* trace_sf, void* stream);
 
+/* ----------------------------------------------------------------- around the attention */
+
+/* A transformer block's steps around the quantized linears and the attention: rotary tables,
+ * the norm and rotation of queries and keys, attention in bf16 under masks, and the output
+ * projection's gated residual.  The pages (Wan2.2 model cards) name the blocks these belong to
+ * -- attn1 / attn2 with normed, rotated queries and keys, and their residual stream -- but no
+ * interface; the formulas are given here.  Inference only: no call has a backward pass. */
+
+/* Rotary table of T tokens: table (device, out) fp32 [T][R], R / 2 pairs
+ *   (c, s) = amplitude (cos, sin)(p f_j),   f_j = theta^(-2 j / d), j < d / 2,
+ * for each position axis in turn (axis a has axis_dims[a] = d dimensions, their sum is R; three
+ * axes for time, height and width of a video, one for text).
+ *   positions  (device) int32 [T][axes]; axes 1 to 4; axis_dims (host) even, R in 2 .. 256
+ *   factor     >= 1: frequencies for a context `factor` times the trained one.  window = 0:
+ *              every f_j / factor.  window > 0 (the trained length): pairs that turn 32 times
+ *              or more within the window keep f_j, pairs that turn once or less take
+ *              f_j / factor, pairs between are blended linearly over j (from the floor of the
+ *              first border, at least 0, to the ceiling of the second, at most d - 1).
+ *   theta      > 1; amplitude > 0 (1, or the factor a scaled model was trained with)
+ * Angles are reduced in 64 bits: a value is within 2^-22 amplitude for |positions| below 2^24, and
+ * within 2^-20 amplitude for all. */
+fp4_status_t fp4_rope_table(const int32_t* positions, int64_t T, int axes, const int64_t* axis_dims, double theta,
+                            double factor, int64_t window, float amplitude, float* table, void* stream);
+
+typedef enum {
+    FP4_NORM_NONE = 0,  /* no norm (weights NULL) */
+    FP4_NORM_HEAD = 1,  /* over each head, weights [D] */
+    FP4_NORM_TOKEN = 2  /* over all heads of a token (Wan2.2's norm_q, norm_k), weights [H D] */
+} fp4_norm_t;
+
+typedef enum {
+    FP4_ROPE_INTERLEAVED = 0, /* pair j is elements 2j, 2j + 1 of the head */
+    FP4_ROPE_HALF = 1         /* pair j is elements j, j + rot / 2 */
+} fp4_rope_layout_t;
+
+/* RMS norm and rotation of queries and keys in one pass over them:
+ *   y = x w / sqrt(mean(x^2) + eps), then each pair (u, v) of the head's first `rot` elements
+ *   becomes (u c - v s, u s + v c); the output is the nearest bf16 of that real number (of one
+ *   within 2^-24 of it, the error of the root).
+ *   q_bf16, k_bf16  (device) [T][H][D] bf16, q_stride / k_stride elements from token to token
+ *                   (>= H D, a multiple of 8: slices of a fused projection do); heads are
+ *                   contiguous.  k_bf16 and k_out NULL: queries alone.  D 64 or 128; the token
+ *                   norm takes H D <= 16384.
+ *   q_weight, k_weight  (device) fp32, 16-byte aligned, or NULL for ones
+ *   eps             >= 0; |x| below 2^62 (squares are summed from fp32 pairs)
+ *   table           (device) fp32 [T][rot] (cos, sin) pairs, e.g. fp4_rope_table's; NULL with rot = 0
+ *   rot             rotated elements of each head, a multiple of 16, at most D
+ *   q_out, k_out    (device, out) bf16, strides as above; q_out may be q_bf16 itself with the
+ *                   same stride (likewise k), other overlaps are not allowed */
+fp4_status_t fp4_qk_norm_rope(const void* q_bf16, int64_t q_stride, int64_t H_q, const void* k_bf16, int64_t k_stride,
+                              int64_t H_k, int64_t T, int64_t D, fp4_norm_t norm, const float* q_weight,
+                              const float* k_weight, float eps, const float* table, int64_t rot,
+                              fp4_rope_layout_t layout, void* q_out, int64_t q_out_stride, void* k_out,
+                              int64_t k_out_stride, void* stream);
+
+/* The same, quantized: exactly the codes and scales that fp4_quantize_heads writes for
+ * fp4_qk_norm_rope's output (head-major layout above, padding tokens included), without that
+ * output's trip through memory.  D = FP4_HEAD_DIM; in the half layout rot is 0, 64 or 128.
+ *   g_q, g_k  (device) NVFP4: the tensors' globals (g_k NULL without keys); MXFP4: NULL */
+fp4_status_t fp4_qk_norm_rope_quantize_heads(fp4_fmt_t fmt, const void* q_bf16, int64_t q_stride, int64_t H_q,
+                                             const void* k_bf16, int64_t k_stride, int64_t H_k, int64_t T, int64_t D,
+                                             fp4_norm_t norm, const float* q_weight, const float* k_weight, float eps,
+                                             const float* table, int64_t rot, fp4_rope_layout_t layout,
+                                             const float* g_q, const float* g_k, uint8_t* q_codes, uint8_t* q_sf,
+                                             uint8_t* k_codes, uint8_t* k_sf, void* stream);
+
+/* Head-major FP4 heads (fp4_quantize_heads, fp4_qk_norm_rope_quantize_heads) back to bf16
+ * [T][H][D], x_stride elements from token to token (>= H D, a multiple of 8): keys of a prompt
+ * that are held in FP4 between steps, read by attention in bf16.  Each value is the nearest bf16
+ * of code * scale (MXFP4, exact) or of fp32(code * fl(scale * g)) (NVFP4; g as given to the
+ * quantizer).  D = FP4_HEAD_DIM. */
+fp4_status_t fp4_dequantize_heads(fp4_fmt_t fmt, const uint8_t* codes, const uint8_t* sf, int64_t T, int64_t H,
+                                  int64_t D, const float* g, void* x_bf16, int64_t x_stride, void* stream);
+
 /* ----------------------------------------------------------------- status */
 
 /* The status calls below are part of this library's error model, not of the method: the

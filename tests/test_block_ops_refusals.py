@@ -1,0 +1,86 @@
+"""Refusals of the operators around the attention, on the host: every invalid call returns its
+status before anything is launched (the addresses are fake and never read)."""
+import ctypes
+
+import pytest
+
+A = 1 << 20          # 16-byte aligned fake address
+BAD = A + 8
+ST = ctypes.c_void_p(0)
+OK, INVALID, SHAPE, MISALIGNED, WORKSPACE = 0, 1, 2, 3, 4
+
+
+@pytest.fixture(scope="module")
+def L():
+    import fp4_block_scaled_act_b200 as fb
+
+    fb.build()
+    return fb.lib()
+
+
+def call(fn, args, **change):
+    args = dict(args)
+    assert set(change) <= set(args)
+    args.update(change)
+    return fn(*args.values(), ST)
+
+
+TABLE = dict(positions=A, T=16, axes=2, dims=(ctypes.c_int64 * 4)(64, 32, 0, 0), theta=1e4, factor=1.0, window=0,
+             amplitude=1.0, table=A)
+
+
+@pytest.mark.parametrize("want,change", [
+    (INVALID, dict(positions=None)), (INVALID, dict(table=None)), (INVALID, dict(dims=None)), (INVALID, dict(T=0)),
+    (INVALID, dict(axes=0)), (INVALID, dict(axes=5)), (INVALID, dict(theta=1.0)), (INVALID, dict(theta=float("nan"))),
+    (INVALID, dict(factor=0.5)), (INVALID, dict(factor=float("inf"))), (INVALID, dict(window=-1)),
+    (INVALID, dict(amplitude=0.0)), (INVALID, dict(amplitude=float("nan"))), (SHAPE, dict(T=1 << 30)),
+    (SHAPE, dict(dims=(ctypes.c_int64 * 4)(63, 32, 0, 0))), (SHAPE, dict(dims=(ctypes.c_int64 * 4)(-2, 32, 0, 0))),
+    (SHAPE, dict(dims=(ctypes.c_int64 * 4)(256, 2, 0, 0))), (SHAPE, dict(dims=(ctypes.c_int64 * 4)(0, 0, 0, 0))),
+    (SHAPE, dict(dims=(ctypes.c_int64 * 4)(1 << 62, 1 << 62, 0, 0))),
+    (MISALIGNED, dict(positions=A + 2)), (MISALIGNED, dict(table=BAD))])
+def test_rope_table_refuses(L, want, change):
+    assert call(L.fp4_rope_table, TABLE, **change) == want
+
+
+ROPE = dict(q=A, q_stride=1024, H_q=8, k=A, k_stride=256, H_k=2, T=16, D=128, norm=1, q_weight=A, k_weight=A, eps=1e-6,
+            table=A, rot=128, layout=0, q_out=A, q_out_stride=1024, k_out=A, k_out_stride=256)
+COMMON = [
+    (INVALID, dict(q=None)), (INVALID, dict(k=None)), (INVALID, dict(T=0)), (INVALID, dict(H_q=0)),
+    (INVALID, dict(H_k=-1)), (INVALID, dict(norm=3)), (INVALID, dict(norm=0)), (INVALID, dict(layout=2)),
+    (INVALID, dict(eps=-1.0)), (INVALID, dict(eps=float("nan"))), (INVALID, dict(table=None)), (INVALID, dict(rot=0)),
+    (INVALID, dict(q_stride=1016)), (INVALID, dict(k_stride=0)), (SHAPE, dict(D=96)), (SHAPE, dict(rot=144)),
+    (SHAPE, dict(rot=24)), (SHAPE, dict(rot=-16)), (SHAPE, dict(T=1 << 30)), (SHAPE, dict(T=1 << 26, q_stride=1024)),
+    (SHAPE, dict(H_q=129, q_stride=1 << 20, norm=2, q_out_stride=1 << 20)), (SHAPE, dict(H_q=1 << 40)),
+    (MISALIGNED, dict(q=BAD)), (MISALIGNED, dict(k=BAD)), (MISALIGNED, dict(q_stride=1028)),
+    (MISALIGNED, dict(k_weight=A + 4)), (MISALIGNED, dict(table=A + 4))]
+
+
+@pytest.mark.parametrize("want,change", COMMON + [
+    (INVALID, dict(q_out=None)), (INVALID, dict(k_out=None)), (INVALID, dict(q_out_stride=512)),
+    (MISALIGNED, dict(q_out=BAD)), (MISALIGNED, dict(k_out_stride=260))])
+def test_norm_rope_refuses(L, want, change):
+    assert call(L.fp4_qk_norm_rope, ROPE, **change) == want
+
+
+QUANT = {**{"fmt": 0}, **{k: v for k, v in ROPE.items() if "_out" not in k}, **dict(
+    g_q=None, g_k=None, q_codes=A, q_sf=A, k_codes=A, k_sf=A)}
+
+
+@pytest.mark.parametrize("want,change", [c for c in COMMON if "q_out_stride" not in c[1]] + [
+    (INVALID, dict(fmt=2)), (INVALID, dict(g_q=A)), (INVALID, dict(fmt=1)), (INVALID, dict(fmt=1, g_q=A)),
+    (INVALID, dict(q_codes=None)), (INVALID, dict(k_sf=None)), (SHAPE, dict(D=64)), (SHAPE, dict(layout=1, rot=32)),
+    (MISALIGNED, dict(q_sf=BAD)), (MISALIGNED, dict(fmt=1, g_q=A, g_k=A + 2))])
+def test_norm_rope_quantize_heads_refuses(L, want, change):
+    assert call(L.fp4_qk_norm_rope_quantize_heads, QUANT, **change) == want
+
+
+DEQUANT = dict(fmt=0, codes=A, sf=A, T=16, H=8, D=128, g=None, x=A, x_stride=1024)
+
+
+@pytest.mark.parametrize("want,change", [
+    (INVALID, dict(fmt=3)), (INVALID, dict(codes=None)), (INVALID, dict(sf=None)), (INVALID, dict(x=None)),
+    (INVALID, dict(T=0)), (INVALID, dict(H=0)), (INVALID, dict(fmt=1)), (INVALID, dict(g=A)),
+    (INVALID, dict(x_stride=1016)), (SHAPE, dict(D=64)), (SHAPE, dict(T=1 << 25)), (MISALIGNED, dict(codes=BAD)),
+    (MISALIGNED, dict(x=BAD)), (MISALIGNED, dict(x_stride=1028)), (MISALIGNED, dict(fmt=1, g=A + 1))])
+def test_dequantize_heads_refuses(L, want, change):
+    assert call(L.fp4_dequantize_heads, DEQUANT, **change) == want
