@@ -1040,19 +1040,18 @@ fp4_status_t w4a4_svd_linear(const void* x_bf16, int64_t M, int64_t K, int64_t N
 namespace {
 inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
-// Persistent launch: a resident wave of blocks at most.
 template <bool TOKEN, int OUT, bool HALF, int D>
 fp4_status_t launch_norm_rope(const DeviceState* ds, const NormRopeParams& p, int tensors, cudaStream_t st) {
-    const auto kernel = norm_rope_kernel<TOKEN, OUT, HALF, D>;
-    const int H = std::max(p.t[0].H, tensors > 1 ? p.t[1].H : 0);
+    const int units = std::max(p.t[0].H, p.t[1].H) * (D / 16);
     const int64_t rows = OUT == NR_BF16 ? p.T : (p.T + 127) / 128 * 128;
-    const int threads = TOKEN ? (H * (D / 16) + 31) / 32 * 32 : 256;
-    const int64_t need = TOKEN ? rows : (rows * H * (D / 16) + 255) / 256;
-    int occ = 0;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, kernel, threads, 0) != cudaSuccess || occ < 1)
-        return FP4_ERR_CUDA;
-    const int64_t blocks = std::min<int64_t>(need, (int64_t)ds->sm_count * occ);
-    kernel<<<dim3((unsigned)blocks, (unsigned)tensors), threads, 0, st>>>(p);
+    // as few warps a token as can hold it; all four of a block where there are too few tokens to
+    // fill the device (one warp would then work alone on 160 values a lane)
+    int wpt = units <= 320 ? 1 : units <= 640 ? 2 : 4;
+    if (rows < (int64_t)ds->sm_count * 4) wpt = 4;
+    const int per = NR_THREADS / 32 / wpt, iters = (units + 32 * wpt - 1) / (32 * wpt);
+    const dim3 grid((unsigned)((rows + per - 1) / per), (unsigned)tensors);
+    // at most 10 units of 32 bytes a lane: 40 KB a block
+    norm_rope_kernel<TOKEN, OUT, HALF, D><<<grid, NR_THREADS, NR_THREADS * iters * 32, st>>>(p, wpt, iters);
     return launched();
 }
 
@@ -1080,10 +1079,8 @@ fp4_status_t check_norm_rope(const NormRopeParams& p, int tensors, int64_t H_q, 
         const int64_t H = i ? H_k : H_q;
         if (!t.x || H < 1) return FP4_ERR_INVALID_ARG;
         if (norm == FP4_NORM_NONE && t.weight) return FP4_ERR_INVALID_ARG;
-        // the token norm keeps a token in one block, 16 values a thread; units are numbered with 32 bits
-        if (H > 16384 / D && norm == FP4_NORM_TOKEN) return FP4_ERR_UNSUPPORTED_SHAPE;
-        if (H >= kMaxDim / D || p.T >= kMaxDim || (p.T + 127) / 128 * 128 * H * (D / 16) >= ((int64_t)1 << 31))
-            return FP4_ERR_UNSUPPORTED_SHAPE;
+        // a token's values are held by one block of four warps, 160 a lane
+        if (H > 16384 / D || p.T >= kMaxDim) return FP4_ERR_UNSUPPORTED_SHAPE;
         if (t.stride < H * D) return FP4_ERR_INVALID_ARG;
         if (!aligned16(t.x) || (t.stride & 7) || !aligned16(t.weight)) return FP4_ERR_MISALIGNED;
     }
@@ -1124,7 +1121,8 @@ fp4_status_t fp4_rope_table(const int32_t* positions, int64_t T, int axes, const
                     window > 0 ? std::min(std::max(((double)j - lo) / std::max(hi - lo, 1e-3), 0.0), 1.0) : 1.0;
                 w = w * (1.0 - ramp) + w / factor * ramp;
             }
-            f.turns[pairs] = w / two_pi;
+            // below 2^64 since w <= 1; in units of 2^-64, from the fp64 quotient
+            f.turns[pairs] = (uint64_t)std::ldexp(w / two_pi, 64);
             f.axis[pairs++] = (int8_t)a;
         }
     }
@@ -1132,7 +1130,8 @@ fp4_status_t fp4_rope_table(const int32_t* positions, int64_t T, int axes, const
     DeviceState* ds;
     fp4_status_t s = device_state(&ds);
     if (s != FP4_OK) return s;
-    const int64_t blocks = std::min<int64_t>((T * pairs + 255) / 256, (int64_t)ds->sm_count * 8);
+    const int64_t per = 256 / pairs;  // tokens per block and step
+    const int64_t blocks = std::min<int64_t>((T + per - 1) / per, (int64_t)ds->sm_count * 8);
     rope_table_kernel<<<(unsigned)blocks, 256, 0, static_cast<cudaStream_t>(stream)>>>(
         positions, T, axes, (int)pairs, amplitude, f, reinterpret_cast<float2*>(table));
     return launched();
@@ -1150,7 +1149,7 @@ fp4_status_t fp4_qk_norm_rope(const void* q_bf16, int64_t q_stride, int64_t H_q,
     const int tensors = k_bf16 ? 2 : 1;
     p.t[0] = {static_cast<const __nv_bfloat16*>(q_bf16), q_stride, (int)H_q, q_weight,
               static_cast<__nv_bfloat16*>(q_out), q_out_stride, nullptr, nullptr, nullptr};
-    p.t[1] = {static_cast<const __nv_bfloat16*>(k_bf16), k_stride, (int)H_k, k_weight,
+    p.t[1] = {static_cast<const __nv_bfloat16*>(k_bf16), k_stride, k_bf16 ? (int)H_k : 0, k_weight,
               static_cast<__nv_bfloat16*>(k_out), k_out_stride, nullptr, nullptr, nullptr};
     fp4_status_t s = check_norm_rope(p, tensors, H_q, H_k, D, norm, eps, layout, 16);
     if (s != FP4_OK) return s;
@@ -1182,7 +1181,7 @@ fp4_status_t fp4_qk_norm_rope_quantize_heads(fp4_fmt_t fmt, const void* q_bf16, 
     p.T = T, p.norm = (int)norm, p.eps = eps, p.table = table, p.rot = (int)rot;
     const int tensors = k_bf16 ? 2 : 1;
     p.t[0] = {static_cast<const __nv_bfloat16*>(q_bf16), q_stride, (int)H_q, q_weight, nullptr, 0, q_codes, q_sf, g_q};
-    p.t[1] = {static_cast<const __nv_bfloat16*>(k_bf16), k_stride, (int)H_k, k_weight, nullptr, 0, k_codes, k_sf, g_k};
+    p.t[1] = {static_cast<const __nv_bfloat16*>(k_bf16), k_stride, k_bf16 ? (int)H_k : 0, k_weight, nullptr, 0, k_codes, k_sf, g_k};
     // in the half layout a block of values lies in neighbouring lanes for rot = 0, 64 and 128
     fp4_status_t s = check_norm_rope(p, tensors, H_q, H_k, D, norm, eps, layout, layout == FP4_ROPE_HALF ? 64 : 16);
     if (s != FP4_OK) return s;
@@ -1200,7 +1199,7 @@ fp4_status_t fp4_dequantize_heads(fp4_fmt_t fmt, const uint8_t* codes, const uin
                                   int64_t D, const float* g, void* x_bf16, int64_t x_stride, void* stream) {
     if (!fmt_ok(fmt) || !codes || !sf || !x_bf16 || T < 1 || H < 1) return FP4_ERR_INVALID_ARG;
     if ((fmt == FP4_FMT_NVFP4) != (g != nullptr)) return FP4_ERR_INVALID_ARG;
-    if (D != FP4_HEAD_DIM || H >= kMaxDim / D || T >= kMaxDim || T * H * 8 >= ((int64_t)1 << 31))
+    if (D != FP4_HEAD_DIM || H > 65535 || T >= kMaxDim)
         return FP4_ERR_UNSUPPORTED_SHAPE;
     if (x_stride < H * D) return FP4_ERR_INVALID_ARG;
     if (!aligned16(codes) || !aligned16(sf) || !aligned16(x_bf16) || (x_stride & 7) || !aligned4(g))
@@ -1208,13 +1207,13 @@ fp4_status_t fp4_dequantize_heads(fp4_fmt_t fmt, const uint8_t* codes, const uin
     DeviceState* ds;
     fp4_status_t s = device_state(&ds);
     if (s != FP4_OK) return s;
-    const int64_t blocks = std::min<int64_t>((T * H * 8 + 255) / 256, (int64_t)ds->sm_count * 8);
+    const dim3 grid((unsigned)((T + 63) / 64), (unsigned)H);
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     const auto out = static_cast<__nv_bfloat16*>(x_bf16);
     if (fmt == FP4_FMT_NVFP4)
-        dequant_heads_kernel<true><<<(unsigned)blocks, 256, 0, st>>>(codes, sf, T, (int)H, g, out, x_stride);
+        dequant_heads_kernel<true><<<grid, 256, 0, st>>>(codes, sf, T, g, out, x_stride);
     else
-        dequant_heads_kernel<false><<<(unsigned)blocks, 256, 0, st>>>(codes, sf, T, (int)H, g, out, x_stride);
+        dequant_heads_kernel<false><<<grid, 256, 0, st>>>(codes, sf, T, g, out, x_stride);
     return launched();
 }
 

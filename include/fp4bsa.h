@@ -501,8 +501,8 @@ typedef enum {
  *   within 2^-24 of it, the error of the root).
  *   q_bf16, k_bf16  (device) [T][H][D] bf16, q_stride / k_stride elements from token to token
  *                   (>= H D, a multiple of 8: slices of a fused projection do); heads are
- *                   contiguous.  k_bf16 and k_out NULL: queries alone.  D 64 or 128; the token
- *                   norm takes H D <= 16384.
+ *                   contiguous.  k_bf16 and k_out NULL: queries alone.  D 64 or 128,
+ *                   H D <= 16384.
  *   q_weight, k_weight  (device) fp32, 16-byte aligned, or NULL for ones
  *   eps             >= 0; |x| below 2^62 (squares are summed from fp32 pairs)
  *   table           (device) fp32 [T][rot] (cos, sin) pairs, e.g. fp4_rope_table's; NULL with rot = 0

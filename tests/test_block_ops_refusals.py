@@ -49,8 +49,8 @@ COMMON = [
     (INVALID, dict(H_k=-1)), (INVALID, dict(norm=3)), (INVALID, dict(norm=0)), (INVALID, dict(layout=2)),
     (INVALID, dict(eps=-1.0)), (INVALID, dict(eps=float("nan"))), (INVALID, dict(table=None)), (INVALID, dict(rot=0)),
     (INVALID, dict(q_stride=1016)), (INVALID, dict(k_stride=0)), (SHAPE, dict(D=96)), (SHAPE, dict(rot=144)),
-    (SHAPE, dict(rot=24)), (SHAPE, dict(rot=-16)), (SHAPE, dict(T=1 << 30)), (SHAPE, dict(T=1 << 26, q_stride=1024)),
-    (SHAPE, dict(H_q=129, q_stride=1 << 20, norm=2, q_out_stride=1 << 20)), (SHAPE, dict(H_q=1 << 40)),
+    (SHAPE, dict(rot=24)), (SHAPE, dict(rot=-16)), (SHAPE, dict(T=1 << 30)),
+    (SHAPE, dict(H_q=129, q_stride=1 << 20, q_out_stride=1 << 20)), (SHAPE, dict(H_q=1 << 40)),
     (MISALIGNED, dict(q=BAD)), (MISALIGNED, dict(k=BAD)), (MISALIGNED, dict(q_stride=1028)),
     (MISALIGNED, dict(k_weight=A + 4)), (MISALIGNED, dict(table=A + 4))]
 
@@ -80,7 +80,8 @@ DEQUANT = dict(fmt=0, codes=A, sf=A, T=16, H=8, D=128, g=None, x=A, x_stride=102
 @pytest.mark.parametrize("want,change", [
     (INVALID, dict(fmt=3)), (INVALID, dict(codes=None)), (INVALID, dict(sf=None)), (INVALID, dict(x=None)),
     (INVALID, dict(T=0)), (INVALID, dict(H=0)), (INVALID, dict(fmt=1)), (INVALID, dict(g=A)),
-    (INVALID, dict(x_stride=1016)), (SHAPE, dict(D=64)), (SHAPE, dict(T=1 << 25)), (MISALIGNED, dict(codes=BAD)),
+    (INVALID, dict(x_stride=1016)), (SHAPE, dict(D=64)), (SHAPE, dict(T=1 << 30)),
+    (SHAPE, dict(H=1 << 16, x_stride=1 << 23)), (MISALIGNED, dict(codes=BAD)),
     (MISALIGNED, dict(x=BAD)), (MISALIGNED, dict(x_stride=1028)), (MISALIGNED, dict(fmt=1, g=A + 1))])
 def test_dequantize_heads_refuses(L, want, change):
     assert call(L.fp4_dequantize_heads, DEQUANT, **change) == want

@@ -273,3 +273,16 @@ def test_capture_other_stream_and_repeat(fb):
     assert torch.equal(qo, fresh[0]) and torch.equal(ko, want[1])
     assert torch.equal(heads[0][0], fb.quantize_heads(fresh[0].reshape(T, -1), H)[0])
     assert torch.equal(back, fb.dequantize_heads(fb.quantize_heads(ko.reshape(T, -1), H), T))
+
+
+def test_infinities_of_unrotated_values_stay_alone(fb):
+    """Without a norm, an infinity in the unrotated part changes no other value."""
+    import torch
+
+    x, table = make(40, 2, 128, 61), make_table(40, 64)
+    for layout in ("interleaved", "half"):
+        y = x.clone()
+        y[3, 1, 70], y[3, 1, 101] = float("inf"), float("-inf")
+        got, clean = (fb.qk_norm_rope(z, norm="none", table=table, layout=layout) for z in (y, x))
+        clean[3, 1, 70], clean[3, 1, 101] = float("inf"), float("-inf")
+        assert torch.equal(got, clean)
