@@ -27,6 +27,9 @@ _FMT = {"mxfp4": MXFP4, "nvfp4": NVFP4, MXFP4: MXFP4, NVFP4: NVFP4}
 NORM_NONE, NORM_HEAD, NORM_TOKEN = 0, 1, 2
 _NORM = {None: NORM_NONE, "none": NORM_NONE, "head": NORM_HEAD, "token": NORM_TOKEN, NORM_NONE: NORM_NONE,
          NORM_HEAD: NORM_HEAD, NORM_TOKEN: NORM_TOKEN}
+ACT_NONE, ACT_GELU_TANH, ACT_SILU = 0, 1, 2
+_ACT = {None: ACT_NONE, "none": ACT_NONE, "gelu_tanh": ACT_GELU_TANH, "silu": ACT_SILU, ACT_NONE: ACT_NONE,
+        ACT_GELU_TANH: ACT_GELU_TANH, ACT_SILU: ACT_SILU}
 ROPE_INTERLEAVED, ROPE_HALF = 0, 1
 _ROPE = {"interleaved": ROPE_INTERLEAVED, "half": ROPE_HALF, ROPE_INTERLEAVED: ROPE_INTERLEAVED, ROPE_HALF: ROPE_HALF}
 
@@ -46,6 +49,7 @@ EXPORTS = [
     "fp4_attn_pv",
     "fp4_attn_fused",
     "fp4_attn_fused_trace",
+    "fp4_gemm_residual", "fp4_linear_residual",
     "fp4_rope_table", "fp4_qk_norm_rope", "fp4_qk_norm_rope_quantize_heads", "fp4_dequantize_heads",
 ]
 
@@ -104,6 +108,8 @@ def lib():
                                    P]),
             "fp4_attn_fused_trace": (I, [I, P, P, I64, P, P, I64, P, P, I64, I64, I64, ctypes.c_float, P, P, P, P, P,
                                          P, I64, P, P, P, P]),
+            "fp4_gemm_residual": (I, [I, P, P, I64, I64, I64, P, P, P, P, P, I, P, I64, P, P, P]),
+            "fp4_linear_residual": (I, [I, P, I64, I64, I64, P, P, P, P, P, I, P, I64, P, P, P, SZ, P]),
             "fp4_rope_table": (I, [P, I64, I, P, D, D, I64, F, P, P]),
             "fp4_qk_norm_rope": (I, [P, I64, I64, P, I64, I64, I64, I64, I, P, P, F, P, I64, I, P, I64, P, I64, P]),
             "fp4_qk_norm_rope_quantize_heads": (I, [I, P, I64, I64, P, I64, I64, I64, I64, I, P, P, F, P, I64, I, P, P,
@@ -341,6 +347,20 @@ def fp4_attn_fused_trace(fmt, q_codes, q_sf, T_q: int, k_codes, k_sf, T_kv: int,
                                       _ptr(vt_codes), _ptr(vt_sf), H, D, head, scale, _ptr(g_q), _ptr(g_k),
                                       _ptr(g_v), _ptr(p_global), _ptr(stats), _ptr(o), trace_tile, _ptr(trace_m),
                                       _ptr(trace_codes), _ptr(trace_sf), _stream(stream)), "fp4_attn_fused_trace")
+
+
+def fp4_gemm_residual(fmt, a_codes, a_sf, M: int, K: int, N: int, w_codes, w_sf, w_global, a_global, bias, act, gate,
+                      gate_rows: int, residual, y, stream=None):
+    _check(lib().fp4_gemm_residual(_fmt(fmt), _ptr(a_codes), _ptr(a_sf), M, K, N, _ptr(w_codes), _ptr(w_sf),
+                                   _ptr(w_global), _ptr(a_global), _ptr(bias), _ACT[act], _ptr(gate), gate_rows,
+                                   _ptr(residual), _ptr(y), _stream(stream)), "fp4_gemm_residual")
+
+
+def fp4_linear_residual(fmt, x, M: int, K: int, N: int, w_codes, w_sf, w_global, a_global, bias, act, gate,
+                        gate_rows: int, residual, y, workspace, ws_bytes: int, stream=None):
+    _check(lib().fp4_linear_residual(_fmt(fmt), _ptr(x), M, K, N, _ptr(w_codes), _ptr(w_sf), _ptr(w_global),
+                                     _ptr(a_global), _ptr(bias), _ACT[act], _ptr(gate), gate_rows, _ptr(residual),
+                                     _ptr(y), _ptr(workspace), ws_bytes, _stream(stream)), "fp4_linear_residual")
 
 
 def fp4_rope_table(positions, T: int, axes: int, axis_dims, theta: float, factor: float, window: int,
@@ -771,6 +791,36 @@ def dequantize_heads(heads, T: int, fmt="mxfp4", g=None, x=None, stream=None):
     with _on(codes.device):
         fp4_dequantize_heads(f, codes, sf, T, H, 2 * half_d, g, x, stride, stream)
     return x
+
+
+def linear_residual(x, pw: PackedWeight, residual=None, bias=None, act="none", gate=None, gate_rows: int = 0,
+                    a_global=None, y=None, workspace=None, stream=None):
+    """residual + gate * act(x W^T + bias) in the GEMM's epilogue: bf16 [M, K] -> bf16 [M, N].  gate: fp32
+    [ceil(M / gate_rows), N], each row for gate_rows rows of y.  y = residual updates it in place."""
+    import torch
+
+    M, K = x.shape
+    N, dev = pw.N, x.device
+    if K != pw.K:
+        raise ValueError(f"x: expected [M, {pw.K}], got {tuple(x.shape)}")
+    _expect(x, "x", torch.bfloat16, dev)
+    _expect(residual, "residual", torch.bfloat16, dev, (M, N))
+    _expect(bias, "bias", torch.float16, dev, (N,))
+    if gate is not None:
+        if gate_rows < 1:
+            raise ValueError("gate_rows: the number of rows of y that share a row of the gate")
+        _expect(gate, "gate", torch.float32, dev, (-(-M // gate_rows), N))
+    _expect(a_global, "a_global", torch.float32, dev)
+    if y is None:
+        y = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+    else:
+        _expect(y, "y", torch.bfloat16, dev, (M, N))
+    if workspace is None:
+        workspace = torch.empty(fp4_linear_workspace_bytes(pw.fmt, M, K, N), dtype=torch.uint8, device=dev)
+    with _on(dev):
+        fp4_linear_residual(pw.fmt, x, M, K, N, pw.codes, pw.sf, pw.w_global, a_global, bias, act, gate,
+                            gate_rows if gate is not None else 0, residual, y, workspace, workspace.numel(), stream)
+    return y
 
 
 class HostPipeline:

@@ -100,6 +100,10 @@ fp4_status_t device_state(DeviceState** out) {
                                      Gemm2Cfg<G_MXFP4, 1>::SMEM_BYTES) != cudaSuccess ||
                 cudaFuncSetAttribute(gemm2_kernel<G_NVFP4, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      Gemm2Cfg<G_NVFP4, 2>::SMEM_BYTES) != cudaSuccess ||
+                cudaFuncSetAttribute(gemm2_kernel<G_MXFP4, OUT_RESIDUAL>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     Gemm2Cfg<G_MXFP4, OUT_RESIDUAL>::SMEM_BYTES) != cudaSuccess ||
+                cudaFuncSetAttribute(gemm2_kernel<G_NVFP4, OUT_RESIDUAL>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     Gemm2Cfg<G_NVFP4, OUT_RESIDUAL>::SMEM_BYTES) != cudaSuccess ||
                 cudaFuncSetAttribute(gemm2_kernel<G_MXFP4, 0, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      Gemm2Cfg<G_MXFP4>::SMEM_BYTES) != cudaSuccess ||
                 cudaFuncSetAttribute(gemm2_kernel<G_NVFP4, 0, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -115,7 +119,9 @@ fp4_status_t device_state(DeviceState** out) {
                     (const void*)gemm2_kernel<G_MXFP4>,          (const void*)gemm2_kernel<G_NVFP4>,
                     (const void*)gemm2_kernel<G_W4A8>,           (const void*)gemm2_kernel<G_SVD4>,
                     (const void*)gemm2_kernel<G_MXFP4, 1>,       (const void*)gemm2_kernel<G_NVFP4, 2>,
-                    (const void*)gemm2_kernel<G_MXFP4, 0, true>, (const void*)gemm2_kernel<G_NVFP4, 0, true>};
+                    (const void*)gemm2_kernel<G_MXFP4, 0, true>, (const void*)gemm2_kernel<G_NVFP4, 0, true>,
+                    (const void*)gemm2_kernel<G_MXFP4, OUT_RESIDUAL>,
+                    (const void*)gemm2_kernel<G_NVFP4, OUT_RESIDUAL>};
                 for (const void* k : pair_kernels)
                     if (!launch_regs_are(k, R)) return FP4_ERR_ARCH;
             }
@@ -379,7 +385,7 @@ fp4_status_t launch_gemm2(const DeviceState* ds, const CUtensorMap& ta, const CU
     // output: bf16 [M, N], stored by the epilogue in 32-row boxes of EPI_COLS columns (64:
     // 128-byte swizzle, 32: 64-byte swizzle)
     CUtensorMap ty = ta;
-    if (OUTQ == 0 && (s = encode_2d(&ty, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.y, (uint64_t)p.N, (uint64_t)p.M,
+    if ((OUTQ == 0 || OUTQ == OUT_RESIDUAL) && (s = encode_2d(&ty, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.y, (uint64_t)p.N, (uint64_t)p.M,
                                     (uint64_t)p.N * 2, C::EPI_COLS, 32,
                                     C::EPI_COLS == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B)) != FP4_OK)
         return s;
@@ -891,6 +897,89 @@ fp4_status_t fp4_linear_gelu_quant(fp4_fmt_t fmt, const void* x_bf16, int64_t M,
     if ((s = fp4_quantize_act(fmt, x_bf16, M, K, a_global, codes, sf, stream)) != FP4_OK) return s;
     return fp4_gemm_gelu_quant(fmt, codes, sf, M, K, N, w_codes, w_sf, w_global, a_global, bias_f16, h_global,
                                h_codes, h_sf, stream);
+}
+
+}  // extern "C"
+namespace {
+// fp4_gemm_residual's arguments (everything but the operands that the quantizer writes)
+fp4_status_t check_residual(fp4_fmt_t fmt, int64_t M, int64_t K, int64_t N, const uint8_t* w_codes,
+                            const uint8_t* w_sf, const float* w_global, const float* a_global, const void* bias_f16,
+                            fp4_act_t act, const float* gate, int64_t gate_rows, const void* residual_bf16,
+                            const void* y_bf16) {
+    if (!fmt_ok(fmt) || !w_codes || !w_sf || !y_bf16) return FP4_ERR_INVALID_ARG;
+    const bool nv = fmt == FP4_FMT_NVFP4;
+    if (nv != (w_global != nullptr) || nv != (a_global != nullptr)) return FP4_ERR_INVALID_ARG;
+    if (act != FP4_ACT_NONE && act != FP4_ACT_GELU_TANH && act != FP4_ACT_SILU) return FP4_ERR_INVALID_ARG;
+    if (gate ? gate_rows < 1 : gate_rows != 0) return FP4_ERR_INVALID_ARG;
+    fp4_status_t s = check_shape(M, K, N);
+    if (s != FP4_OK) return s;
+    if (!aligned16(w_codes) || !aligned16(w_sf) || !aligned16(y_bf16) || !aligned16(bias_f16) || !aligned16(gate) ||
+        (reinterpret_cast<uintptr_t>(residual_bf16) & 31u) || (reinterpret_cast<uintptr_t>(w_global) & 3u) ||
+        (reinterpret_cast<uintptr_t>(a_global) & 3u))
+        return FP4_ERR_MISALIGNED;
+    return FP4_OK;
+}
+
+fp4_status_t gemm_residual_impl(fp4_fmt_t fmt, const uint8_t* a_codes, const uint8_t* a_sf, int64_t M, int64_t K,
+                                int64_t N, const uint8_t* w_codes, const uint8_t* w_sf, const float* w_global,
+                                const float* a_global, const void* bias_f16, fp4_act_t act, const float* gate,
+                                int64_t gate_rows, const void* residual_bf16, void* y_bf16, void* stream, bool pdl) {
+    if (!a_codes || !a_sf) return FP4_ERR_INVALID_ARG;
+    fp4_status_t s = check_residual(fmt, M, K, N, w_codes, w_sf, w_global, a_global, bias_f16, act, gate, gate_rows,
+                                    residual_bf16, y_bf16);
+    if (s != FP4_OK) return s;
+    if (!aligned16(a_codes) || !aligned16(a_sf)) return FP4_ERR_MISALIGNED;
+    DeviceState* ds;
+    if ((s = device_state(&ds)) != FP4_OK) return s;
+    // always the 2-CTA kernel
+    CUtensorMap ta, tb;
+    if ((s = encode_2d(&ta, CU_TENSOR_MAP_DATA_TYPE_UINT8, a_codes, K / 2, M, K / 2, 128, GEMM_BM)) != FP4_OK)
+        return s;
+    if ((s = encode_2d(&tb, CU_TENSOR_MAP_DATA_TYPE_UINT8, w_codes, K / 2, N, K / 2, 128, 128)) != FP4_OK) return s;
+    GemmParams p{};
+    p.M = (int)M, p.N = (int)N, p.K = (int)K;
+    p.sfa = a_sf, p.sfb = w_sf, p.g_a = a_global, p.g_w = w_global;
+    p.bias = static_cast<const __half*>(bias_f16);
+    p.y = static_cast<__nv_bfloat16*>(y_bf16);
+    p.act = (int)act, p.gate = gate;
+    p.gate_rows = (int)std::min<int64_t>(gate_rows, M);  // M rows and more: one row of the gate
+    p.res = static_cast<const __nv_bfloat16*>(residual_bf16);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return fmt == FP4_FMT_NVFP4
+               ? launch_gemm2<G_NVFP4, OUT_RESIDUAL>(ds, ta, tb, a_sf, w_sf, p, st, nullptr, nullptr, pdl)
+               : launch_gemm2<G_MXFP4, OUT_RESIDUAL>(ds, ta, tb, a_sf, w_sf, p, st, nullptr, nullptr, pdl);
+}
+}  // namespace
+
+extern "C" {
+
+fp4_status_t fp4_gemm_residual(fp4_fmt_t fmt, const uint8_t* a_codes, const uint8_t* a_sf, int64_t M, int64_t K,
+                               int64_t N, const uint8_t* w_codes, const uint8_t* w_sf, const float* w_global,
+                               const float* a_global, const void* bias_f16, fp4_act_t act, const float* gate,
+                               int64_t gate_rows, const void* residual_bf16, void* y_bf16, void* stream) {
+    return gemm_residual_impl(fmt, a_codes, a_sf, M, K, N, w_codes, w_sf, w_global, a_global, bias_f16, act, gate,
+                              gate_rows, residual_bf16, y_bf16, stream, false);
+}
+
+fp4_status_t fp4_linear_residual(fp4_fmt_t fmt, const void* x_bf16, int64_t M, int64_t K, int64_t N,
+                                 const uint8_t* w_codes, const uint8_t* w_sf, const float* w_global,
+                                 const float* a_global, const void* bias_f16, fp4_act_t act, const float* gate,
+                                 int64_t gate_rows, const void* residual_bf16, void* y_bf16, void* workspace,
+                                 size_t ws_bytes, void* stream) {
+    if (!x_bf16 || !workspace) return FP4_ERR_INVALID_ARG;
+    // everything is validated before the quantizer is launched
+    fp4_status_t s = check_residual(fmt, M, K, N, w_codes, w_sf, w_global, a_global, bias_f16, act, gate, gate_rows,
+                                    residual_bf16, y_bf16);
+    if (s != FP4_OK) return s;
+    if (ws_bytes < fp4_linear_workspace_bytes(fmt, M, K, N)) return FP4_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return FP4_ERR_MISALIGNED;
+    uint8_t* codes = static_cast<uint8_t*>(workspace);
+    uint8_t* sf = codes + align256(fp4_codes_bytes(fmt, M, K));
+    if ((s = fp4_quantize_act(fmt, x_bf16, M, K, a_global, codes, sf, stream)) != FP4_OK) return s;
+    // as fp4_linear: short GEMMs overlap their launch with the quantizer, which reads x alone
+    const bool pdl = g_pdl != 0 && ((M + 255) / 256) * ((N + 255) / 256) <= 2 * kPlanPairs;
+    return gemm_residual_impl(fmt, codes, sf, M, K, N, w_codes, w_sf, w_global, a_global, bias_f16, act, gate,
+                              gate_rows, residual_bf16, y_bf16, stream, pdl);
 }
 
 }  // extern "C"

@@ -73,6 +73,10 @@ struct GemmParams {
     uint8_t* h_codes;         // fused GELU + quantize output: FP4 codes [M, N/2]
     uint8_t* h_sf;            //   and scale bytes (128x4 atoms over [M, N])
     const float* g_h;         //   NVFP4 global of that output (device scalar) or null
+    int act;                  // gated residual output: fp4_act_t (0 none, 1 GELU-tanh, 2 SiLU)
+    const float* gate;        //   fp32 [ceil(M / gate_rows)][N] or null
+    int gate_rows;            //   rows that share a row of the gate
+    const __nv_bfloat16* res; //   residual [M, N] or null
     int seg_max;              // stream-K (2-CTA kernel): partial slabs per tile in `partials`
     float* partials;          //   fp32 [tiles][seg_max][256][256] partial sums of split tiles
     int* counters;            //   [tiles][16] arrivals per 32 x 128 region (zero before launch)
@@ -130,6 +134,75 @@ FP4_DEV void epilogue_store(const GemmParams& p, uint32_t (&acc)[NC][32], int ro
         for (int g = 0; g < 4; ++g)
             *reinterpret_cast<uint4*>(yrow + c * 32 + g * 8) =
                 make_uint4(acc[c][4 * g], acc[c][4 * g + 1], acc[c][4 * g + 2], acc[c][4 * g + 3]);
+}
+
+// Gated residual epilogue: 64 columns of one row, as epilogue_pack, but
+//   y = bf16_rn(res + gate * act(acc gs + bias))
+// with everything after the accumulator in fp32 and one rounding (gate * act + res is one fma).
+// res: the row's 64 residual values, loaded ahead (ld_residual).
+FP4_DEV void act_x2(int act, float& a, float& b) {
+    if (act == 1) {
+        gelu_f32_x2(a, b, a, b);
+    } else if (act == 2) {  // z / (1 + exp(-z)); exp overflows to infinity, whose reciprocal is 0
+        a *= __frcp_rn(1.0f + exp2f(a * -1.44269504f));
+        b *= __frcp_rn(1.0f + exp2f(b * -1.44269504f));
+    }
+}
+FP4_DEV void ld_residual(const GemmParams& p, int row, int col0, uint32_t (&res)[4][8]) {
+    if (p.res && row < p.M && col0 < p.N) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) ld_global_v8(p.res + (size_t)row * p.N + col0 + 16 * i, res[i]);
+    }
+}
+FP4_DEV void epilogue_pack_residual(const GemmParams& p, uint32_t (&acc)[2][32], const uint32_t (&res)[4][8], int row,
+                                    int col0, float gs) {
+    const float* gate = p.gate ? p.gate + (size_t)(row / p.gate_rows) * p.N + col0 : nullptr;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+#pragma unroll
+        for (int j = 0; j < 32; j += 8) {
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = __fmul_rn(__uint_as_float(acc[c][j + i]), gs);
+            if (p.bias) {
+                const uint4 bv = __ldg(reinterpret_cast<const uint4*>(p.bias + col0 + c * 32 + j));
+                const __half2* bh = reinterpret_cast<const __half2*>(&bv);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 bf = __half22float2(bh[i]);
+                    v[2 * i] = __fmaf_rn(__uint_as_float(acc[c][j + 2 * i]), gs, bf.x);
+                    v[2 * i + 1] = __fmaf_rn(__uint_as_float(acc[c][j + 2 * i + 1]), gs, bf.y);
+                }
+            }
+            if (p.act) {
+#pragma unroll
+                for (int i = 0; i < 8; i += 2) act_x2(p.act, v[i], v[i + 1]);
+            }
+            float g[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) g[i] = 1.0f;
+            if (gate) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float4 f = __ldg(reinterpret_cast<const float4*>(gate + c * 32 + j + 4 * i));
+                    g[4 * i] = f.x, g[4 * i + 1] = f.y, g[4 * i + 2] = f.z, g[4 * i + 3] = f.w;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t w = res[(c * 32 + j) / 16][(j % 16) / 2 + i];
+                float lo, hi;
+                if (p.res) {
+                    lo = __fmaf_rn(g[2 * i], v[2 * i], __uint_as_float(w << 16));
+                    hi = __fmaf_rn(g[2 * i + 1], v[2 * i + 1], __uint_as_float(w & 0xFFFF0000u));
+                } else {
+                    lo = g[2 * i] * v[2 * i], hi = g[2 * i + 1] * v[2 * i + 1];
+                }
+                const __nv_bfloat162 b2 = __floats2bfloat162_rn(lo, hi);
+                acc[c][j / 2 + i] = *reinterpret_cast<const uint32_t*>(&b2);
+            }
+        }
+    }
 }
 
 // Which TMEM scale atom and which byte of it MMA number k of a stage reads.
@@ -411,6 +484,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
 //   acc_free[b]  (leader)  accumulator b fully drained by both CTAs (16 warps)
 //   ovl_free     (leader)  overlap columns of the last tile drained (8 warps)
 // =======================================================================================
+constexpr int OUT_RESIDUAL = 3;  // OUTQ value, see gemm2_kernel
 // named barrier of the 8 epilogue warps (the MMA hand-off ring uses ids 1 .. TB <= 4)
 constexpr uint32_t EPI_TABLE_BAR = 8;
 
@@ -499,15 +573,11 @@ struct Gemm2Cfg {
     static_assert(OVL == 64 || OVL == 96, "epilogue overlap handling");
 };
 
-// Pair-kernel epilogue: pack one row's 64 columns and write them, as 128 bytes, into row
-// `r` of the warp's 32 x 128-byte staging tile in the 128-byte-swizzled layout the output
-// tensor map reads (16-byte granule g of row r at granule g ^ (r % 8)).  Rows at or beyond
-// M are not computed; the TMA store clips them.
-template <int KIND>
-FP4_DEV void epilogue_stage(const GemmParams& p, uint32_t (&acc)[2][32], int row, int col0, float gs, uint8_t* tile,
-                            int r) {
-    if (row >= p.M) return;
-    epilogue_pack<KIND, 2>(p, acc, row, col0, gs);
+// Pair-kernel epilogue: write one row's 64 packed columns, 128 bytes, into row `r` of the
+// warp's 32 x 128-byte staging tile in the 128-byte-swizzled layout the output tensor map
+// reads (16-byte granule g of row r at granule g ^ (r % 8)).  Rows at or beyond M are not
+// computed; the TMA store clips them.
+FP4_DEV void epilogue_stage_64(const uint32_t (&acc)[2][32], uint8_t* tile, int r) {
     const uint32_t base = smem_u32(tile) + (uint32_t)r * 128u;
 #pragma unroll
     for (int c = 0; c < 2; ++c)
@@ -650,7 +720,8 @@ FP4_DEV void arrive_leader_relaxed(uint64_t* bar, uint32_t rank) {
 }
 
 // OUTQ 0: bf16 output through the TMA-store epilogue; 1 / 2: the fused GELU + MXFP4 /
-// NVFP4 quantize epilogue (epilogue_gelu_quant) in place of the bf16 output.
+// NVFP4 quantize epilogue (epilogue_gelu_quant) in place of the bf16 output; OUT_RESIDUAL:
+// bf16 output through activation, gate and residual (epilogue_pack_residual).
 // SK: the stream-K schedule (small problems, opt-in); a separate instantiation so the
 // default kernel carries none of its registers.
 template <int KIND, int OUTQ = 0, bool SK = false>
@@ -788,6 +859,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Gemm2Cfg<KIND>::THRE
         for (; sc.get(tile, kb0, kb1); sc.step(kb0, kb1), ++tcount) {
             const int mb = tile / num_n, nb = tile % num_n;
             const int b = tcount & 1;
+            const int row0 = mb * 256 + (int)rank * 128 + q * 32;
+            const int row = row0 + lane;
+            const int col0 = nb * GEMM_BN + h * 128;
+            // the 64-column half drained first (see below), and the other
+            const bool holds_overlap = (h == (b == 0 ? 1 : 0));
+            const int first = holds_overlap ? (b == 0 ? 2 : 0) : 0;
+            const int second = 2 - first;
+            [[maybe_unused]] uint32_t res[4][8];  // residual values of the half drained next
+            if (OUTQ == OUT_RESIDUAL) ld_residual(p, row, col0 + first * 32, res);
             const bool got = mbar_wait(&tmem_full[b], ((uint32_t)tcount >> 1) & 1u, p.timeout_ns, abort);
             if (!__all_sync(0xffffffffu, got)) {
                 if (lane == 0) gemm2_fail(p, abort, peer_abort);
@@ -796,9 +876,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Gemm2Cfg<KIND>::THRE
             tc_fence_after();
             const uint32_t taddr =
                 tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * C::ACC1_COL) + (uint32_t)(h * 128);
-            const int row0 = mb * 256 + (int)rank * 128 + q * 32;
-            const int row = row0 + lane;
-            const int col0 = nb * GEMM_BN + h * 128;
             // stream-K: the tile's segments (pairs whose share meets it) and this unit's index
             int nseg = 1, seg = 0;
             if constexpr (SK) {
@@ -814,15 +891,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Gemm2Cfg<KIND>::THRE
             // pack 64 columns into the staging tile and hand them to one TMA store (which
             // clips rows at or beyond M); the tile is reused once the previous store has read it
             auto emit = [&](uint32_t (&a)[2][32], int chunk) {
-                if (OUTQ != 0) {
+                if constexpr (OUTQ == 1 || OUTQ == 2) {
                     epilogue_gelu_quant<KIND, OUTQ>(p, a, row, col0 + chunk * 32, gs, g_h, six_g_h, rcp_tab);
                     return;
                 }
                 if (col0 >= p.N) return;
                 if constexpr (C::EPI_COLS == 64) {
+                    if constexpr (OUTQ == OUT_RESIDUAL) {
+                        if (row < p.M) epilogue_pack_residual(p, a, res, row, col0 + chunk * 32, gs);
+                        // the other half's residual is on its way while this half is stored
+                        if (chunk == first) ld_residual(p, row, col0 + second * 32, res);
+                    }
                     if (lane == 0) bulk_wait_group_read0();
                     __syncwarp();
-                    epilogue_stage<KIND>(p, a, row, col0 + chunk * 32, gs, stile, lane);
+                    if (row < p.M) {
+                        if constexpr (OUTQ == 0) epilogue_pack<KIND, 2>(p, a, row, col0 + chunk * 32, gs);
+                        epilogue_stage_64(a, stile, lane);
+                    }
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0 && row0 < p.M) {
@@ -865,9 +950,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Gemm2Cfg<KIND>::THRE
             // accumulator 0 (half 1) or the first OVL of accumulator 1 (half 0): their holders
             // drain them first and release them -- after the first chunk pair when OVL = 64,
             // after copying all four chunks with HOLD_ALL, else after both pairs
-            const bool holds_overlap = (h == (b == 0 ? 1 : 0));
-            const int first = holds_overlap ? (b == 0 ? 2 : 0) : 0;
-            const int second = 2 - first;
             tmem_ld_32x32b_x32(taddr + first * 32, acc[0]);
             tmem_ld_32x32b_x32(taddr + (first + 1) * 32, acc[1]);
             if (C::HOLD_ALL && holds_overlap) {

@@ -303,6 +303,15 @@ FP4_DEV void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t (&v)[16]) {
 }
 FP4_DEV void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// ------------------------------------------------------------------ plain loads
+// 32 bytes per thread (32-byte aligned): one whole sector a lane.
+FP4_DEV void ld_global_v8(const void* p, uint32_t (&r)[8]) {
+    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "l"(p)
+                 : "memory");
+}
+
 // ------------------------------------------------------------------ conversions
 // Eight fp32 values -> eight E2M1 codes in one 32-bit word (value i in nibble i),
 // hardware round-to-nearest-even with saturation.

@@ -237,6 +237,36 @@ fp4_status_t fp4_linear_gelu_quant(fp4_fmt_t fmt, const void* x_bf16, int64_t M,
                                    uint8_t* h_codes, uint8_t* h_sf, void* workspace,
                                    size_t ws_bytes, void* stream);
 
+/* ----------------------------------------------------------------- gated residual */
+
+typedef enum {
+    FP4_ACT_NONE = 0,
+    FP4_ACT_GELU_TANH = 1, /* evaluated in fp32 as described above, not rounded to bf16 */
+    FP4_ACT_SILU = 2       /* z / (1 + exp(-z)) */
+} fp4_act_t;
+
+/* A block's output projection with what follows it (Wan2.2 blocks: x + proj(h) * gate, the gate
+ * from the time embedding), in the GEMM's epilogue instead of a pass over [M, N] of its own:
+ *   y[m,n] = bf16_rn( residual[m,n] + gate[m / gate_rows, n] * act( acc[m,n] + bias[n] ) )
+ * with acc as fp4_gemm's sum; all of it in fp32, rounded once.
+ *   act            activation
+ *   gate           (device) fp32 [ceil(M / gate_rows)][N]: one row for gate_rows rows of y (a
+ *                  clip's tokens; 1: a gate per token), or NULL with gate_rows = 0 (a gate of 1)
+ *   residual_bf16  (device) [M, N] bf16, 32-byte aligned, or NULL (0); y_bf16 may be the same
+ *                  memory (not any other overlap)
+ * Other arguments as fp4_gemm.  Always the 2-CTA kernel. */
+fp4_status_t fp4_gemm_residual(fp4_fmt_t fmt, const uint8_t* a_codes, const uint8_t* a_sf, int64_t M, int64_t K,
+                               int64_t N, const uint8_t* w_codes, const uint8_t* w_sf, const float* w_global,
+                               const float* a_global, const void* bias_f16, fp4_act_t act, const float* gate,
+                               int64_t gate_rows, const void* residual_bf16, void* y_bf16, void* stream);
+
+/* fp4_quantize_act of x into `workspace` (fp4_linear_workspace_bytes), then fp4_gemm_residual. */
+fp4_status_t fp4_linear_residual(fp4_fmt_t fmt, const void* x_bf16, int64_t M, int64_t K, int64_t N,
+                                 const uint8_t* w_codes, const uint8_t* w_sf, const float* w_global,
+                                 const float* a_global, const void* bias_f16, fp4_act_t act, const float* gate,
+                                 int64_t gate_rows, const void* residual_bf16, void* y_bf16, void* workspace,
+                                 size_t ws_bytes, void* stream);
+
 /* ----------------------------------------------------------------- W4A8 SVDQuant */
 
 /* Activation side of the W4A8 SVDQuant linear (W4A8 README, W4A8 format: the activations

@@ -85,3 +85,29 @@ DEQUANT = dict(fmt=0, codes=A, sf=A, T=16, H=8, D=128, g=None, x=A, x_stride=102
     (MISALIGNED, dict(x=BAD)), (MISALIGNED, dict(x_stride=1028)), (MISALIGNED, dict(fmt=1, g=A + 1))])
 def test_dequantize_heads_refuses(L, want, change):
     assert call(L.fp4_dequantize_heads, DEQUANT, **change) == want
+
+
+GEMM = dict(fmt=0, a_codes=A, a_sf=A, M=16, K=256, N=256, w_codes=A, w_sf=A, w_global=None, a_global=None, bias=A, act=0,
+            gate=A, gate_rows=16, residual=A, y=A)
+RESIDUAL = [
+    (INVALID, dict(fmt=2)), (INVALID, dict(w_codes=None)), (INVALID, dict(w_sf=None)), (INVALID, dict(y=None)),
+    (INVALID, dict(w_global=A)), (INVALID, dict(fmt=1)), (INVALID, dict(fmt=1, w_global=A)), (INVALID, dict(act=3)),
+    (INVALID, dict(gate_rows=0)), (INVALID, dict(gate=None)), (INVALID, dict(M=0)), (SHAPE, dict(K=200)),
+    (SHAPE, dict(N=192)), (SHAPE, dict(M=1 << 30)), (MISALIGNED, dict(residual=A + 16)), (MISALIGNED, dict(y=BAD)),
+    (MISALIGNED, dict(gate=A + 4)), (MISALIGNED, dict(bias=A + 2)), (MISALIGNED, dict(w_sf=BAD))]
+
+
+@pytest.mark.parametrize("want,change", RESIDUAL + [(INVALID, dict(a_codes=None)), (INVALID, dict(a_sf=None)),
+                                                    (MISALIGNED, dict(a_sf=BAD))])
+def test_gemm_residual_refuses(L, want, change):
+    assert call(L.fp4_gemm_residual, GEMM, **change) == want
+
+
+LINEAR = {("x" if k == "a_codes" else k): v for k, v in GEMM.items() if k != "a_sf"} | dict(workspace=A, ws_bytes=1 << 30)
+
+
+@pytest.mark.parametrize("want,change", RESIDUAL + [(INVALID, dict(x=None)), (INVALID, dict(workspace=None)),
+                                                    (WORKSPACE, dict(ws_bytes=100)), (MISALIGNED, dict(x=BAD)),
+                                                    (MISALIGNED, dict(workspace=BAD))])
+def test_linear_residual_refuses(L, want, change):
+    assert call(L.fp4_linear_residual, LINEAR, **change) == want
