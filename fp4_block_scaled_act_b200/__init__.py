@@ -51,6 +51,7 @@ EXPORTS = [
     "fp4_attn_fused_trace",
     "fp4_gemm_residual", "fp4_linear_residual",
     "fp4_rope_table", "fp4_qk_norm_rope", "fp4_qk_norm_rope_quantize_heads", "fp4_dequantize_heads",
+    "fp4_attn_bf16_workspace_bytes", "fp4_attn_bf16", "fp4_attn_ranges",
 ]
 
 
@@ -115,6 +116,10 @@ def lib():
             "fp4_qk_norm_rope_quantize_heads": (I, [I, P, I64, I64, P, I64, I64, I64, I64, I, P, P, F, P, I64, I, P, P,
                                                     P, P, P, P, P]),
             "fp4_dequantize_heads": (I, [I, P, P, I64, I64, I64, P, P, I64, P]),
+            "fp4_attn_bf16_workspace_bytes": (SZ, [I64, I64, I64, I64, I64]),
+            "fp4_attn_bf16": (I, [P, I64, I64, P, I64, P, I64, I64, I64, I64, I64, F, F, P, I64, P, P, P, I64, P, P, SZ,
+                                  P]),
+            "fp4_attn_ranges": (I, [P, P, I64, I64, I64, I, P, P, P, P]),
             "fp4_sync_status": (I, [P]),
             "fp4_status_string": (ctypes.c_char_p, [I]),
             "fp4_set_wait_timeout_ns": (None, [ctypes.c_uint64]),
@@ -395,6 +400,26 @@ def fp4_dequantize_heads(fmt, codes, sf, T: int, H: int, D: int, g, x, x_stride:
     """x may be rows of a larger buffer (x_stride in elements)."""
     _check(lib().fp4_dequantize_heads(_fmt(fmt), _ptr(codes), _ptr(sf), T, H, D, _ptr(g), _rows_ptr(x), x_stride,
                                       _stream(stream)), "fp4_dequantize_heads")
+
+
+def fp4_attn_bf16_workspace_bytes(T_q: int, T_kv: int, H: int, H_kv: int, D: int = 128) -> int:
+    return lib().fp4_attn_bf16_workspace_bytes(T_q, T_kv, H, H_kv, D)
+
+
+def fp4_attn_bf16(q, q_stride: int, T_q: int, k, k_stride: int, v, v_stride: int, T_kv: int, H: int, H_kv: int, D: int,
+                  scale: float, softcap: float, slopes, q_pos: int, key_start, key_end, o, o_stride: int, lse,
+                  workspace, ws_bytes: int, stream=None):
+    """q, k, v and o may be rows of larger buffers (strides in elements)."""
+    _check(lib().fp4_attn_bf16(_rows_ptr(q), q_stride, T_q, _rows_ptr(k), k_stride, _rows_ptr(v), v_stride, T_kv, H,
+                               H_kv, D, scale, softcap, _ptr(slopes), q_pos, _ptr(key_start), _ptr(key_end),
+                               _rows_ptr(o), o_stride, _ptr(lse), _ptr(workspace), ws_bytes, _stream(stream)),
+           "fp4_attn_bf16")
+
+
+def fp4_attn_ranges(q_offsets, k_offsets, docs: int, T_q: int, T_kv: int, causal, prefix, key_start, key_end,
+                    stream=None):
+    _check(lib().fp4_attn_ranges(_ptr(q_offsets), _ptr(k_offsets), docs, T_q, T_kv, int(bool(causal)), _ptr(prefix),
+                                 _ptr(key_start), _ptr(key_end), _stream(stream)), "fp4_attn_ranges")
 
 
 def fp4_sync_status(stream=None) -> int:
@@ -821,6 +846,55 @@ def linear_residual(x, pw: PackedWeight, residual=None, bias=None, act="none", g
         fp4_linear_residual(pw.fmt, x, M, K, N, pw.codes, pw.sf, pw.w_global, a_global, bias, act, gate,
                             gate_rows if gate is not None else 0, residual, y, workspace, workspace.numel(), stream)
     return y
+
+
+def attn_ranges(q_offsets, k_offsets, T_q: int, T_kv: int, causal=False, prefix=None, stream=None):
+    """Key ranges (key_start, key_end), int32 [T_q], of documents packed on the query and key axes (int32
+    offsets [docs + 1], CUDA), in causal order or not, each with a prefix (int32 [docs]) that all its rows see."""
+    import torch
+
+    dev, docs = q_offsets.device, q_offsets.numel() - 1
+    _expect(q_offsets, "q_offsets", torch.int32, dev, (docs + 1,))
+    _expect(k_offsets, "k_offsets", torch.int32, dev, (docs + 1,))
+    _expect(prefix, "prefix", torch.int32, dev, (docs,))
+    ranges = torch.empty((2, T_q), dtype=torch.int32, device=dev)
+    with _on(dev):
+        fp4_attn_ranges(q_offsets, k_offsets, docs, T_q, T_kv, causal, prefix, ranges[0], ranges[1], stream)
+    return ranges[0], ranges[1]
+
+
+def attn_bf16(q, k, v, scale: float, softcap: float = 0.0, slopes=None, q_pos: int = 0, key_start=None, key_end=None,
+              o=None, return_lse=False, workspace=None, stream=None):
+    """Attention of bf16 q [T_q, H, D] over k, v [T_kv, H_kv, D] (slices of fused projections do): bf16
+    [T_q, H, D], and with return_lse its fp32 log-sum-exp [T_q, H].  softcap > 0 caps the scores by a tanh,
+    slopes (fp32 [H]) times the distance |q_pos + i - j| is taken from them, and row i sees the keys
+    key_start[i] <= j < key_end[i] (int32 [T_q]; None: from the first, to the last)."""
+    import torch
+
+    strides = [_expect_rows(t, what, q.device) for t, what in ((q, "q"), (k, "k"), (v, "v"))]
+    dev = q.device
+    T_q, H, D = q.shape
+    T_kv, H_kv, _ = k.shape
+    if k.shape != v.shape or k.shape[2] != D:
+        raise ValueError(f"k, v: expected [T_kv, H_kv, {D}], got {tuple(k.shape)}, {tuple(v.shape)}")
+    _expect(slopes, "slopes", torch.float32, dev, (H,))
+    _expect(key_start, "key_start", torch.int32, dev, (T_q,))
+    _expect(key_end, "key_end", torch.int32, dev, (T_q,))
+    if o is None:
+        o = torch.empty((T_q, H, D), dtype=torch.bfloat16, device=dev)
+    o_stride = _expect_rows(o, "o", dev)
+    if o.shape != q.shape:
+        raise ValueError(f"o: expected {tuple(q.shape)}, got {tuple(o.shape)}")
+    lse = torch.empty((T_q, H), dtype=torch.float32, device=dev) if return_lse else None
+    ws = fp4_attn_bf16_workspace_bytes(T_q, T_kv, H, H_kv, D)
+    if workspace is None and ws:
+        workspace = torch.empty(ws, dtype=torch.uint8, device=dev)
+    _expect(workspace, "workspace", torch.uint8, dev)
+    with _on(dev):
+        fp4_attn_bf16(q, strides[0], T_q, k, strides[1], v, strides[2], T_kv, H, H_kv, D, scale, softcap, slopes, q_pos,
+                      key_start, key_end, o, o_stride, lse, workspace, workspace.numel() if workspace is not None else 0,
+                      stream)
+    return (o, lse) if return_lse else o
 
 
 class HostPipeline:

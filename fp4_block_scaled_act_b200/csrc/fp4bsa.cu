@@ -10,6 +10,7 @@
 
 #include "fp4bsa.h"
 #include "attn.cuh"
+#include "attn_bf16.cuh"
 #include "attn_fused.cuh"
 #include "gemm.cuh"
 #include "norm_rope.cuh"
@@ -113,6 +114,20 @@ fp4_status_t device_state(DeviceState** out) {
                 cudaFuncSetAttribute(attn_fused_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      ATT_SMEM) != cudaSuccess)
                 return FP4_ERR_CUDA;
+            {
+                const void* attn_kernels[] = {
+                    (const void*)attn_bf16_kernel<64, false, false>,  (const void*)attn_bf16_kernel<64, false, true>,
+                    (const void*)attn_bf16_kernel<64, true, false>,   (const void*)attn_bf16_kernel<64, true, true>,
+                    (const void*)attn_bf16_kernel<128, false, false>, (const void*)attn_bf16_kernel<128, false, true>,
+                    (const void*)attn_bf16_kernel<128, true, false>,  (const void*)attn_bf16_kernel<128, true, true>};
+                for (int i = 0; i < 8; ++i) {
+                    // the softmax warps' register increase is sized for exactly this launch
+                    if (!launch_regs_are(attn_kernels[i], (int)AB_REG_LAUNCH)) return FP4_ERR_ARCH;
+                    if (cudaFuncSetAttribute(attn_kernels[i], cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             i < 4 ? AttnBfCfg<64>::SMEM : AttnBfCfg<128>::SMEM) != cudaSuccess)
+                        return FP4_ERR_CUDA;
+                }
+            }
             {
                 constexpr int R = (int)Gemm2Cfg<G_MXFP4>::REG_LAUNCH;
                 const void* pair_kernels[] = {
@@ -250,6 +265,45 @@ fp4_status_t encode_2d(CUtensorMap* m, CUtensorMapDataType dt, const void* ptr, 
                           swz, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return FP4_ERR_CUDA;
+    const int slot = (c.n < kTmapCache) ? c.n++ : (c.next++ % kTmapCache);
+    c.key[slot] = key;
+    c.map[slot] = *m;
+    return FP4_OK;
+}
+
+// A [tokens][heads][D] bf16 tensor, `stride` elements from token to token, in boxes of 64 columns x
+// box_heads heads x box_tokens tokens (128-byte swizzle); cached like the 2-D maps.
+struct HeadsTmapKey {
+    const void* ptr;
+    int64_t D, heads, tokens, stride;
+    uint32_t box_heads, box_tokens;
+    bool operator==(const HeadsTmapKey& o) const {
+        return ptr == o.ptr && D == o.D && heads == o.heads && tokens == o.tokens && stride == o.stride &&
+               box_heads == o.box_heads && box_tokens == o.box_tokens;
+    }
+};
+struct HeadsTmapCache {
+    HeadsTmapKey key[kTmapCache];
+    CUtensorMap map[kTmapCache];
+    int n = 0, next = 0;
+};
+thread_local HeadsTmapCache t_heads_tmaps;
+
+fp4_status_t encode_heads(CUtensorMap* m, const HeadsTmapKey& key) {
+    HeadsTmapCache& c = t_heads_tmaps;
+    for (int i = 0; i < c.n; ++i)
+        if (c.key[i] == key) {
+            *m = c.map[i];
+            return FP4_OK;
+        }
+    const cuuint64_t dims[3] = {(cuuint64_t)key.D, (cuuint64_t)key.heads, (cuuint64_t)key.tokens};
+    const cuuint64_t strides[2] = {(cuuint64_t)key.D * 2, (cuuint64_t)key.stride * 2};
+    const cuuint32_t box[3] = {64, key.box_heads, key.box_tokens};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    if (g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(key.ptr), dims, strides, box, estr,
+                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return FP4_ERR_CUDA;
     const int slot = (c.n < kTmapCache) ? c.n++ : (c.next++ % kTmapCache);
     c.key[slot] = key;
     c.map[slot] = *m;
@@ -1303,6 +1357,135 @@ fp4_status_t fp4_dequantize_heads(fp4_fmt_t fmt, const uint8_t* codes, const uin
         dequant_heads_kernel<true><<<grid, 256, 0, st>>>(codes, sf, T, g, out, x_stride);
     else
         dequant_heads_kernel<false><<<grid, 256, 0, st>>>(codes, sf, T, g, out, x_stride);
+    return launched();
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------------------
+// Attention in bf16
+namespace {
+constexpr int kPlanSMs = 148;  // workspaces are sized for a B200
+
+int attn_bf16_tokens(int64_t H, int64_t H_kv) { return (int)(128 / (H / H_kv)); }
+
+// How many parts the keys are split into: one where the row tiles alone fill the device, else as
+// many as fill it once, each of two key tiles at least (a part costs a prologue and its share of
+// the join: T_q = 1 over 100,001 keys x 8 key heads takes 18 parts).
+int attn_bf16_splits(int64_t T_q, int64_t T_kv, int64_t H, int64_t H_kv) {
+    const int64_t rows = 2 * attn_bf16_tokens(H, H_kv);
+    const int64_t ctas = (T_q + rows - 1) / rows * H_kv, tiles = (T_kv + 127) / 128;
+    return (int)std::max<int64_t>(1, std::min<int64_t>(kPlanSMs / std::min<int64_t>(ctas, kPlanSMs), tiles / 2));
+}
+
+fp4_status_t check_attn_bf16(int64_t T_q, int64_t T_kv, int64_t H, int64_t H_kv, int64_t D) {
+    if (T_q < 1 || T_kv < 1 || H < 1 || H_kv < 1) return FP4_ERR_INVALID_ARG;
+    if ((D != 64 && D != 128) || H % H_kv != 0 || H / H_kv > 128) return FP4_ERR_UNSUPPORTED_SHAPE;
+    if (T_q >= kMaxDim || T_kv >= kMaxDim || H >= kMaxDim / D) return FP4_ERR_UNSUPPORTED_SHAPE;
+    const int64_t rows = 2 * attn_bf16_tokens(H, H_kv);
+    if ((T_q + rows - 1) / rows * H_kv >= ((int64_t)1 << 31)) return FP4_ERR_UNSUPPORTED_SHAPE;
+    return FP4_OK;
+}
+
+template <int D>
+fp4_status_t launch_attn_bf16(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                              const AttnBfParams& p, bool cap, cudaStream_t st) {
+    const dim3 grid((unsigned)(p.q_tiles * p.H_kv), 1, (unsigned)p.splits);
+    constexpr int SM = AttnBfCfg<D>::SMEM;
+    if (cap && p.slopes)
+        attn_bf16_kernel<D, true, true><<<grid, AB_THREADS, SM, st>>>(tq, tk, tv, p);
+    else if (cap)
+        attn_bf16_kernel<D, true, false><<<grid, AB_THREADS, SM, st>>>(tq, tk, tv, p);
+    else if (p.slopes)
+        attn_bf16_kernel<D, false, true><<<grid, AB_THREADS, SM, st>>>(tq, tk, tv, p);
+    else
+        attn_bf16_kernel<D, false, false><<<grid, AB_THREADS, SM, st>>>(tq, tk, tv, p);
+    if (p.splits == 1) return launched();
+    fp4_status_t s = launched();
+    if (s != FP4_OK) return s;
+    const int64_t rows = (int64_t)p.T_q * p.H;
+    attn_bf16_join_kernel<D><<<(unsigned)((rows + 3) / 4), 128, 0, st>>>(p);
+    return launched();
+}
+}  // namespace
+
+extern "C" {
+
+size_t fp4_attn_bf16_workspace_bytes(int64_t T_q, int64_t T_kv, int64_t H, int64_t H_kv, int64_t D) {
+    if (check_attn_bf16(T_q, T_kv, H, H_kv, D) != FP4_OK) return 0;
+    const int64_t sp = attn_bf16_splits(T_q, T_kv, H, H_kv);
+    if (sp == 1) return 0;
+    return align256((size_t)sp * T_q * H * D * 4) + align256((size_t)sp * T_q * H * 8);
+}
+
+fp4_status_t fp4_attn_bf16(const void* q_bf16, int64_t q_stride, int64_t T_q, const void* k_bf16, int64_t k_stride,
+                           const void* v_bf16, int64_t v_stride, int64_t T_kv, int64_t H, int64_t H_kv, int64_t D,
+                           float scale, float softcap, const float* slopes, int64_t q_pos, const int32_t* key_start,
+                           const int32_t* key_end, void* o_bf16, int64_t o_stride, float* lse, void* workspace,
+                           size_t ws_bytes, void* stream) {
+    if (!q_bf16 || !k_bf16 || !v_bf16 || !o_bf16) return FP4_ERR_INVALID_ARG;
+    if (!(scale > 0.0f) || !(scale < 1.0e30f) || !(softcap >= 0.0f) || !(softcap < 1.0e30f)) return FP4_ERR_INVALID_ARG;
+    if (q_pos <= -((int64_t)1 << 40) || q_pos >= ((int64_t)1 << 40)) return FP4_ERR_INVALID_ARG;
+    fp4_status_t s = check_attn_bf16(T_q, T_kv, H, H_kv, D);
+    if (s != FP4_OK) return s;
+    if (q_stride < H * D || k_stride < H_kv * D || v_stride < H_kv * D || o_stride < H * D) return FP4_ERR_INVALID_ARG;
+    // (a tensor map takes strides below 2^40 bytes)
+    constexpr int64_t kMaxStride = (int64_t)1 << 38;
+    if (q_stride >= kMaxStride || k_stride >= kMaxStride || v_stride >= kMaxStride || o_stride >= kMaxStride)
+        return FP4_ERR_UNSUPPORTED_SHAPE;
+    if (!aligned16(q_bf16) || !aligned16(k_bf16) || !aligned16(v_bf16) || !aligned16(o_bf16) || !aligned4(slopes) ||
+        !aligned4(key_start) || !aligned4(key_end) || !aligned4(lse) || ((q_stride | k_stride | v_stride | o_stride) & 7))
+        return FP4_ERR_MISALIGNED;
+    const int splits = attn_bf16_splits(T_q, T_kv, H, H_kv);
+    if (splits > 1) {
+        if (!workspace) return FP4_ERR_INVALID_ARG;
+        if (ws_bytes < fp4_attn_bf16_workspace_bytes(T_q, T_kv, H, H_kv, D)) return FP4_ERR_WORKSPACE;
+        if (!aligned16(workspace)) return FP4_ERR_MISALIGNED;
+    }
+    DeviceState* ds;
+    if ((s = device_state(&ds)) != FP4_OK) return s;
+    AttnBfParams p{};
+    p.T_q = (int)T_q, p.T_kv = (int)T_kv, p.H = (int)H, p.H_kv = (int)H_kv, p.g = (int)(H / H_kv);
+    p.tokens = attn_bf16_tokens(H, H_kv);
+    p.q_tiles = (int)((T_q + 2 * p.tokens - 1) / (2 * p.tokens)), p.splits = splits;
+    // masked calls: the row tiles of all heads together, the last (in causal order the longest)
+    // first, so that the short ones fill the gaps; else a head's row tiles together, whose keys
+    // then stay in L2
+    p.heads_first = key_start || key_end;
+    const double log2e = 1.4426950408889634;
+    p.c = (float)(softcap > 0.0f ? 2.0 * scale * log2e / softcap : scale * log2e);
+    p.cap = (float)(softcap * log2e);
+    p.slopes = slopes, p.q_pos = q_pos, p.key_start = key_start, p.key_end = key_end;
+    p.v = static_cast<const __nv_bfloat16*>(v_bf16), p.v_stride = v_stride;
+    p.o = static_cast<__nv_bfloat16*>(o_bf16), p.o_stride = o_stride, p.lse = lse;
+    if (splits > 1) {
+        p.part_o = static_cast<float*>(workspace);
+        p.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + align256((size_t)splits * T_q * H * D * 4));
+    }
+    p.timeout_ns = g_timeout_ns;
+    p.status = ds->status;
+    CUtensorMap tq, tk, tv;
+    if ((s = encode_heads(&tq, {q_bf16, D, H, T_q, q_stride, (uint32_t)p.g, (uint32_t)p.tokens})) != FP4_OK) return s;
+    if ((s = encode_heads(&tk, {k_bf16, D, H_kv, T_kv, k_stride, 1, 128})) != FP4_OK) return s;
+    if ((s = encode_heads(&tv, {v_bf16, D, H_kv, T_kv, v_stride, 1, 128})) != FP4_OK) return s;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return D == 128 ? launch_attn_bf16<128>(tq, tk, tv, p, softcap > 0.0f, st)
+                    : launch_attn_bf16<64>(tq, tk, tv, p, softcap > 0.0f, st);
+}
+
+fp4_status_t fp4_attn_ranges(const int32_t* q_offsets, const int32_t* k_offsets, int64_t docs, int64_t T_q,
+                             int64_t T_kv, int causal, const int32_t* prefix, int32_t* key_start, int32_t* key_end,
+                             void* stream) {
+    if (!q_offsets || !k_offsets || !key_start || !key_end || docs < 1 || T_q < 1 || T_kv < 1)
+        return FP4_ERR_INVALID_ARG;
+    if (docs >= kMaxDim || T_q >= kMaxDim || T_kv >= kMaxDim) return FP4_ERR_UNSUPPORTED_SHAPE;
+    if (!aligned4(q_offsets) || !aligned4(k_offsets) || !aligned4(prefix) || !aligned4(key_start) || !aligned4(key_end))
+        return FP4_ERR_MISALIGNED;
+    DeviceState* ds;
+    fp4_status_t s = device_state(&ds);
+    if (s != FP4_OK) return s;
+    attn_ranges_kernel<<<(unsigned)((T_q + 255) / 256), 256, 0, static_cast<cudaStream_t>(stream)>>>(
+        q_offsets, k_offsets, (int)docs, (int)T_q, (int)T_kv, causal != 0, prefix, key_start, key_end);
     return launched();
 }
 

@@ -564,6 +564,48 @@ fp4_status_t fp4_qk_norm_rope_quantize_heads(fp4_fmt_t fmt, const void* q_bf16, 
 fp4_status_t fp4_dequantize_heads(fp4_fmt_t fmt, const uint8_t* codes, const uint8_t* sf, int64_t T, int64_t H,
                                   int64_t D, const float* g, void* x_bf16, int64_t x_stride, void* stream);
 
+/* Attention in bf16, all heads in one call, with shared key heads and masks: for the attention
+ * layers that a model keeps unquantized, and for those that need what fp4_attn_fused has not.
+ * Query row i, head h reads key head h / (H / H_kv):
+ *   s_ij = scale (q_i . k_j);   softcap > 0:  s_ij = softcap tanh(s_ij / softcap);
+ *   slopes:  s_ij -= slopes[h] |q_pos + i - j|;
+ *   o_i = sum_j p_ij v_j / sum_j p_ij with p_ij = exp(s_ij - max_j s_ij) over the keys
+ *   key_start[i] <= j < key_end[i] (cut to 0 .. T_kv), lse_i = log sum_j exp(s_ij).
+ * A row that sees no key gives o = 0 and lse = -infinity.  A row's result depends on no key or
+ * value outside its range, whatever these hold (infinities and NaN among them).
+ *   q_bf16   (device) [T_q][H][D] bf16, q_stride elements from token to token; k_bf16, v_bf16
+ *            (device) [T_kv][H_kv][D] with k_stride, v_stride; o_bf16 (device, out) [T_q][H][D] with
+ *            o_stride.  Strides are at least a token's elements and multiples of 8 (slices of
+ *            a fused projection do).  D 64 or 128; H a multiple of H_kv, at most 128 times it.
+ *   scale    > 0; softcap >= 0 (0: none)
+ *   slopes   (device) fp32 [H] or NULL; q_pos: position of query row 0 on the keys' axis
+ *   key_start, key_end  (device) int32 [T_q], or NULL for 0 and for T_kv (fp4_attn_ranges makes
+ *            them for documents, causal order and prefixes)
+ *   lse      (device, out) fp32 [T_q][H], or NULL
+ *   workspace  (device) at least fp4_attn_bf16_workspace_bytes; may be NULL where that is 0.  With
+ *            few query rows the keys are split over CTAs and joined from it.  Calls that may run
+ *            at the same time need their own.
+ * Arithmetic: products of bf16 with fp32 sums on the tensor cores, the softmax in fp32 and its
+ * weights rounded to bf16 for the second product (their sum is taken before that rounding).
+ * Deterministic. */
+size_t fp4_attn_bf16_workspace_bytes(int64_t T_q, int64_t T_kv, int64_t H, int64_t H_kv, int64_t D);
+fp4_status_t fp4_attn_bf16(const void* q_bf16, int64_t q_stride, int64_t T_q, const void* k_bf16, int64_t k_stride,
+                           const void* v_bf16, int64_t v_stride, int64_t T_kv, int64_t H, int64_t H_kv, int64_t D,
+                           float scale, float softcap, const float* slopes, int64_t q_pos, const int32_t* key_start,
+                           const int32_t* key_end, void* o_bf16, int64_t o_stride, float* lse, void* workspace,
+                           size_t ws_bytes, void* stream);
+
+/* Key ranges of documents packed one after another: query rows q_offsets[d] .. q_offsets[d+1] - 1
+ * belong to document d, whose keys are k_offsets[d] .. k_offsets[d+1] - 1.  A row sees its
+ * document's keys; with causal != 0 those up to its own place (the last query row of a document
+ * stands at its last key), or the first prefix[d] where that is more.  Rows of no document, and
+ * rows before their document's first key, see none (key_start = key_end).
+ *   q_offsets, k_offsets  (device) int32 [docs + 1], not decreasing; prefix (device) int32 [docs] or NULL
+ *   key_start, key_end    (device, out) int32 [T_q] */
+fp4_status_t fp4_attn_ranges(const int32_t* q_offsets, const int32_t* k_offsets, int64_t docs, int64_t T_q,
+                             int64_t T_kv, int causal, const int32_t* prefix, int32_t* key_start, int32_t* key_end,
+                             void* stream);
+
 /* ----------------------------------------------------------------- status */
 
 /* The status calls below are part of this library's error model, not of the method: the

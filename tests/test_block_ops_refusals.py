@@ -111,3 +111,45 @@ LINEAR = {("x" if k == "a_codes" else k): v for k, v in GEMM.items() if k != "a_
                                                     (MISALIGNED, dict(workspace=BAD))])
 def test_linear_residual_refuses(L, want, change):
     assert call(L.fp4_linear_residual, LINEAR, **change) == want
+
+
+ATTN = dict(q=A, q_stride=1024, T_q=16, k=A, k_stride=256, v=A, v_stride=256, T_kv=16, H=8, H_kv=2, D=128, scale=0.1,
+            softcap=0.0, slopes=None, q_pos=0, key_start=None, key_end=None, o=A, o_stride=1024, lse=None, workspace=None,
+            ws_bytes=0)
+
+
+@pytest.mark.parametrize("want,change", [
+    (INVALID, dict(q=None)), (INVALID, dict(k=None)), (INVALID, dict(v=None)), (INVALID, dict(o=None)),
+    (INVALID, dict(T_q=0)), (INVALID, dict(T_kv=0)), (INVALID, dict(H=0)), (INVALID, dict(H_kv=0)),
+    (INVALID, dict(scale=0.0)), (INVALID, dict(scale=float("nan"))), (INVALID, dict(softcap=-1.0)),
+    (INVALID, dict(softcap=float("inf"))), (INVALID, dict(q_stride=1016)), (INVALID, dict(k_stride=128)),
+    (INVALID, dict(v_stride=0)), (INVALID, dict(o_stride=8)), (INVALID, dict(q_pos=1 << 41)), (SHAPE, dict(D=96)),
+    (SHAPE, dict(H=9, q_stride=4096, o_stride=4096)), (SHAPE, dict(H=258, q_stride=1 << 20, o_stride=1 << 20)),
+    (SHAPE, dict(T_q=1 << 30)), (SHAPE, dict(T_kv=1 << 30)), (SHAPE, dict(k_stride=1 << 38)), (MISALIGNED, dict(q=BAD)),
+    (MISALIGNED, dict(o=BAD)), (MISALIGNED, dict(v_stride=260)), (MISALIGNED, dict(lse=A + 2)),
+    (MISALIGNED, dict(key_end=A + 2)), (INVALID, dict(T_kv=100000)), (WORKSPACE, dict(T_kv=100000, workspace=A)),
+    (MISALIGNED, dict(T_kv=100000, workspace=BAD, ws_bytes=1 << 30))])
+def test_attn_bf16_refuses(L, want, change):
+    assert call(L.fp4_attn_bf16, ATTN, **change) == want
+
+
+def test_attn_bf16_workspace_sizes(L):
+    f = L.fp4_attn_bf16_workspace_bytes
+    assert f(75600, 75600, 40, 40, 128) == 0            # the row tiles fill the device
+    assert f(1, 256, 8, 8, 128) == 0                     # two key tiles: one part
+    # 8 key heads: 18 parts of 148 SMs; O parts, then (maximum, sum) pairs
+    assert f(1, 100001, 40, 8, 128) == 18 * 40 * 128 * 4 + (18 * 40 * 8 + 255) // 256 * 256
+    for bad in ((0, 1, 1, 1, 64), (1, 0, 1, 1, 64), (1, 1, 3, 2, 64), (1, 1, 1, 1, 32), (1 << 30, 1, 1, 1, 64)):
+        assert f(*bad) == 0
+
+
+RANGES = dict(q_offsets=A, k_offsets=A, docs=2, T_q=16, T_kv=16, causal=1, prefix=None, key_start=A, key_end=A)
+
+
+@pytest.mark.parametrize("want,change", [
+    (INVALID, dict(q_offsets=None)), (INVALID, dict(k_offsets=None)), (INVALID, dict(key_start=None)),
+    (INVALID, dict(key_end=None)), (INVALID, dict(docs=0)), (INVALID, dict(T_q=0)), (INVALID, dict(T_kv=0)),
+    (SHAPE, dict(docs=1 << 30)), (SHAPE, dict(T_q=1 << 30)), (MISALIGNED, dict(prefix=A + 1)),
+    (MISALIGNED, dict(key_end=A + 2))])
+def test_attn_ranges_refuses(L, want, change):
+    assert call(L.fp4_attn_ranges, RANGES, **change) == want
