@@ -1369,13 +1369,21 @@ constexpr int kPlanSMs = 148;  // workspaces are sized for a B200
 
 int attn_bf16_tokens(int64_t H, int64_t H_kv) { return (int)(128 / (H / H_kv)); }
 
-// How many parts the keys are split into: one where the row tiles alone fill the device, else as
-// many as fill it once, each of two key tiles at least (a part costs a prologue and its share of
-// the join: T_q = 1 over 100,001 keys x 8 key heads takes 18 parts).
+// Few rows, one row tile a key head: the two row tiles of an item take its even and odd key tiles
+// (two parts), so that it has two key tiles to work on at once.
+bool attn_bf16_alt(int64_t T_q, int64_t T_kv, int64_t H, int64_t H_kv) {
+    return T_q <= attn_bf16_tokens(H, H_kv) && T_kv > AB_KEYS;
+}
+// How many items the keys of a row tile pair are split into: one where the row tiles alone fill the
+// device, else as many as fill it once, each of two key tiles at least (a part costs a prologue
+// and its share of the join: T_q = 1 over 100,001 keys x 8 key heads takes 18).
 int attn_bf16_splits(int64_t T_q, int64_t T_kv, int64_t H, int64_t H_kv) {
     const int64_t rows = 2 * attn_bf16_tokens(H, H_kv);
-    const int64_t ctas = (T_q + rows - 1) / rows * H_kv, tiles = (T_kv + 127) / 128;
+    const int64_t ctas = (T_q + rows - 1) / rows * H_kv, tiles = (T_kv + AB_KEYS - 1) / AB_KEYS;
     return (int)std::max<int64_t>(1, std::min<int64_t>(kPlanSMs / std::min<int64_t>(ctas, kPlanSMs), tiles / 2));
+}
+int attn_bf16_parts(int64_t T_q, int64_t T_kv, int64_t H, int64_t H_kv) {
+    return attn_bf16_splits(T_q, T_kv, H, H_kv) * (attn_bf16_alt(T_q, T_kv, H, H_kv) ? 2 : 1);
 }
 
 fp4_status_t check_attn_bf16(int64_t T_q, int64_t T_kv, int64_t H, int64_t H_kv, int64_t D) {
@@ -1383,14 +1391,14 @@ fp4_status_t check_attn_bf16(int64_t T_q, int64_t T_kv, int64_t H, int64_t H_kv,
     if ((D != 64 && D != 128) || H % H_kv != 0 || H / H_kv > 128) return FP4_ERR_UNSUPPORTED_SHAPE;
     if (T_q >= kMaxDim || T_kv >= kMaxDim || H >= kMaxDim / D) return FP4_ERR_UNSUPPORTED_SHAPE;
     const int64_t rows = 2 * attn_bf16_tokens(H, H_kv);
-    if ((T_q + rows - 1) / rows * H_kv >= ((int64_t)1 << 31)) return FP4_ERR_UNSUPPORTED_SHAPE;
+    if ((T_q + rows - 1) / rows * H_kv >= ((int64_t)1 << 30)) return FP4_ERR_UNSUPPORTED_SHAPE;
     return FP4_OK;
 }
 
 template <int D>
-fp4_status_t launch_attn_bf16(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+fp4_status_t launch_attn_bf16(const DeviceState* ds, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                               const AttnBfParams& p, bool cap, cudaStream_t st) {
-    const dim3 grid((unsigned)(p.q_tiles * p.H_kv), 1, (unsigned)p.splits);
+    const unsigned grid = (unsigned)std::min(p.items, ds->sm_count);
     constexpr int SM = AttnBfCfg<D>::SMEM;
     if (cap && p.slopes)
         attn_bf16_kernel<D, true, true><<<grid, AB_THREADS, SM, st>>>(tq, tk, tv, p);
@@ -1400,7 +1408,7 @@ fp4_status_t launch_attn_bf16(const CUtensorMap& tq, const CUtensorMap& tk, cons
         attn_bf16_kernel<D, false, true><<<grid, AB_THREADS, SM, st>>>(tq, tk, tv, p);
     else
         attn_bf16_kernel<D, false, false><<<grid, AB_THREADS, SM, st>>>(tq, tk, tv, p);
-    if (p.splits == 1) return launched();
+    if (p.parts == 1) return launched();
     fp4_status_t s = launched();
     if (s != FP4_OK) return s;
     const int64_t rows = (int64_t)p.T_q * p.H;
@@ -1413,9 +1421,9 @@ extern "C" {
 
 size_t fp4_attn_bf16_workspace_bytes(int64_t T_q, int64_t T_kv, int64_t H, int64_t H_kv, int64_t D) {
     if (check_attn_bf16(T_q, T_kv, H, H_kv, D) != FP4_OK) return 0;
-    const int64_t sp = attn_bf16_splits(T_q, T_kv, H, H_kv);
-    if (sp == 1) return 0;
-    return align256((size_t)sp * T_q * H * D * 4) + align256((size_t)sp * T_q * H * 8);
+    const int64_t parts = attn_bf16_parts(T_q, T_kv, H, H_kv);
+    if (parts == 1) return 0;
+    return align256((size_t)parts * T_q * H * D * 4) + align256((size_t)parts * T_q * H * 8);
 }
 
 fp4_status_t fp4_attn_bf16(const void* q_bf16, int64_t q_stride, int64_t T_q, const void* k_bf16, int64_t k_stride,
@@ -1436,8 +1444,8 @@ fp4_status_t fp4_attn_bf16(const void* q_bf16, int64_t q_stride, int64_t T_q, co
     if (!aligned16(q_bf16) || !aligned16(k_bf16) || !aligned16(v_bf16) || !aligned16(o_bf16) || !aligned4(slopes) ||
         !aligned4(key_start) || !aligned4(key_end) || !aligned4(lse) || ((q_stride | k_stride | v_stride | o_stride) & 7))
         return FP4_ERR_MISALIGNED;
-    const int splits = attn_bf16_splits(T_q, T_kv, H, H_kv);
-    if (splits > 1) {
+    const int splits = attn_bf16_splits(T_q, T_kv, H, H_kv), parts = attn_bf16_parts(T_q, T_kv, H, H_kv);
+    if (parts > 1) {
         if (!workspace) return FP4_ERR_INVALID_ARG;
         if (ws_bytes < fp4_attn_bf16_workspace_bytes(T_q, T_kv, H, H_kv, D)) return FP4_ERR_WORKSPACE;
         if (!aligned16(workspace)) return FP4_ERR_MISALIGNED;
@@ -1447,30 +1455,33 @@ fp4_status_t fp4_attn_bf16(const void* q_bf16, int64_t q_stride, int64_t T_q, co
     AttnBfParams p{};
     p.T_q = (int)T_q, p.T_kv = (int)T_kv, p.H = (int)H, p.H_kv = (int)H_kv, p.g = (int)(H / H_kv);
     p.tokens = attn_bf16_tokens(H, H_kv);
-    p.q_tiles = (int)((T_q + 2 * p.tokens - 1) / (2 * p.tokens)), p.splits = splits;
+    p.q_tiles = (int)((T_q + 2 * p.tokens - 1) / (2 * p.tokens)), p.splits = splits, p.parts = parts;
+    p.alt = attn_bf16_alt(T_q, T_kv, H, H_kv);
+    p.items = (int)(p.q_tiles * H_kv * splits);
     // masked calls: the row tiles of all heads together, the last (in causal order the longest)
     // first, so that the short ones fill the gaps; else a head's row tiles together, whose keys
     // then stay in L2
     p.heads_first = key_start || key_end;
     const double log2e = 1.4426950408889634;
-    p.c = (float)(softcap > 0.0f ? 2.0 * scale * log2e / softcap : scale * log2e);
+    p.c = (float)(softcap > 0.0f ? (double)scale / softcap : scale * log2e);
     p.cap = (float)(softcap * log2e);
     p.slopes = slopes, p.q_pos = q_pos, p.key_start = key_start, p.key_end = key_end;
     p.v = static_cast<const __nv_bfloat16*>(v_bf16), p.v_stride = v_stride;
     p.o = static_cast<__nv_bfloat16*>(o_bf16), p.o_stride = o_stride, p.lse = lse;
-    if (splits > 1) {
+    p.o_32 = ((reinterpret_cast<uintptr_t>(o_bf16) | (uintptr_t)(o_stride * 2)) & 31u) == 0;
+    if (parts > 1) {
         p.part_o = static_cast<float*>(workspace);
-        p.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + align256((size_t)splits * T_q * H * D * 4));
+        p.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + align256((size_t)parts * T_q * H * D * 4));
     }
     p.timeout_ns = g_timeout_ns;
     p.status = ds->status;
     CUtensorMap tq, tk, tv;
     if ((s = encode_heads(&tq, {q_bf16, D, H, T_q, q_stride, (uint32_t)p.g, (uint32_t)p.tokens})) != FP4_OK) return s;
-    if ((s = encode_heads(&tk, {k_bf16, D, H_kv, T_kv, k_stride, 1, 128})) != FP4_OK) return s;
-    if ((s = encode_heads(&tv, {v_bf16, D, H_kv, T_kv, v_stride, 1, 128})) != FP4_OK) return s;
+    if ((s = encode_heads(&tk, {k_bf16, D, H_kv, T_kv, k_stride, 1, AB_KEYS})) != FP4_OK) return s;
+    if ((s = encode_heads(&tv, {v_bf16, D, H_kv, T_kv, v_stride, 1, AB_KEYS})) != FP4_OK) return s;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    return D == 128 ? launch_attn_bf16<128>(tq, tk, tv, p, softcap > 0.0f, st)
-                    : launch_attn_bf16<64>(tq, tk, tv, p, softcap > 0.0f, st);
+    return D == 128 ? launch_attn_bf16<128>(ds, tq, tk, tv, p, softcap > 0.0f, st)
+                    : launch_attn_bf16<64>(ds, tq, tk, tv, p, softcap > 0.0f, st);
 }
 
 fp4_status_t fp4_attn_ranges(const int32_t* q_offsets, const int32_t* k_offsets, int64_t docs, int64_t T_q,

@@ -312,6 +312,12 @@ FP4_DEV void ld_global_v8(const void* p, uint32_t (&r)[8]) {
                  : "memory");
 }
 
+FP4_DEV void st_global_v8(void* p, const uint32_t (&r)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+                 "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+
 // ------------------------------------------------------------------ conversions
 // Eight fp32 values -> eight E2M1 codes in one 32-bit word (value i in nibble i),
 // hardware round-to-nearest-even with saturation.

@@ -136,9 +136,9 @@ def test_attn_bf16_refuses(L, want, change):
 def test_attn_bf16_workspace_sizes(L):
     f = L.fp4_attn_bf16_workspace_bytes
     assert f(75600, 75600, 40, 40, 128) == 0            # the row tiles fill the device
-    assert f(1, 256, 8, 8, 128) == 0                     # two key tiles: one part
-    # 8 key heads: 18 parts of 148 SMs; O parts, then (maximum, sum) pairs
-    assert f(1, 100001, 40, 8, 128) == 18 * 40 * 128 * 4 + (18 * 40 * 8 + 255) // 256 * 256
+    assert f(1, 128, 8, 8, 128) == 0                     # one key tile: one part
+    # 8 key heads on 148 SMs: 18 items each, two parts an item; O parts, then (maximum, sum) pairs
+    assert f(1, 100001, 40, 8, 128) == 36 * 40 * 128 * 4 + (36 * 40 * 8 + 255) // 256 * 256
     for bad in ((0, 1, 1, 1, 64), (1, 0, 1, 1, 64), (1, 1, 3, 2, 64), (1, 1, 1, 1, 32), (1 << 30, 1, 1, 1, 64)):
         assert f(*bad) == 0
 
