@@ -12,7 +12,6 @@ allocate outputs and workspaces with torch and call the same entry points.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 from dataclasses import dataclass
@@ -164,8 +163,9 @@ def _stream(stream=None):
     import torch
 
     if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+        # (the current stream's handle without a Stream object around it: a few microseconds a call)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _check(status: int, where: str):
@@ -679,38 +679,48 @@ def linear_gelu_quant(x, pw: PackedWeight, bias=None, a_global=None, h_global=No
 
 
 # ----------------------------------------------------------------------------- around the attention
-# These helpers check types, shapes and devices, since the C calls see only addresses.
-def _expect(t, what: str, dtype, device, shape=None):
-    """t is a contiguous CUDA tensor of this type on this device (and of this shape), or None."""
+# These helpers check types, shapes and devices, since the C calls see only addresses, and hand on
+# addresses, so that nothing is checked twice: for small calls the host's time is what counts.
+def _expect(t, what: str, dtype, dev: int, shape=None):
+    """Address of t, which has to be a contiguous tensor of this type on CUDA device `dev` (and of this
+    shape); None for None."""
     if t is None:
-        return
-    if t.dtype != dtype or t.device != device:
-        raise ValueError(f"{what}: expected {dtype} on {device}, got {t.dtype} on {t.device}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+        return None
+    if t.dtype != dtype or t.get_device() != dev or dev < 0:
+        raise ValueError(f"{what}: expected {dtype} on cuda:{max(dev, 0)}, got {t.dtype} on {t.device}")
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{what}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{what}: expected a contiguous tensor")
+    return t.data_ptr()
 
 
-def _expect_rows(t, what: str, device=None):
-    """t is a bf16 CUDA tensor [T, H, D] with contiguous heads; returns its row stride in elements."""
+def _expect_rows(t, what: str, dev: int, shape=None):
+    """(address, row stride in elements) of t, which has to be a bf16 tensor [T, H, D] with contiguous heads on
+    CUDA device `dev` (and of this shape)."""
     import torch
 
-    if t.dim() != 3 or t.dtype != torch.bfloat16 or not t.is_cuda:
-        raise ValueError(f"{what}: expected a bf16 CUDA tensor [T, H, D], got {t.dtype} {tuple(t.shape)} on {t.device}")
-    if device is not None and t.device != device:
-        raise ValueError(f"{what}: expected a tensor on {device}, got {t.device}")
+    if t.dim() != 3 or t.dtype != torch.bfloat16 or t.get_device() != dev or dev < 0:
+        raise ValueError(f"{what}: expected a bf16 CUDA tensor [T, H, D] on cuda:{max(dev, 0)}, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{what}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
     T, H, D = t.shape
-    if t.stride(2) != 1 or (H > 1 and t.stride(1) != D):
+    row, head, one = t.stride()
+    if one != 1 or (H > 1 and head != D):
         raise ValueError(f"{what}: heads must be contiguous (strides {t.stride()})")
-    return t.stride(0) if T > 1 else H * D
+    return t.data_ptr(), row if T > 1 else H * D
 
 
-def _on(device):
-    """Context in which the launches go to the tensors' device."""
+def _launch(dev: int, call, *args):
+    """The call with CUDA device `dev` current (its stream is that device's current one)."""
     import torch
 
-    return contextlib.nullcontext() if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+    if torch.cuda.current_device() == dev:
+        call(*args)
+    else:
+        with torch.cuda.device(dev):
+            call(*args)
 
 
 def rope_table(positions, axis_dims, theta: float = 10000.0, factor: float = 1.0, window: int = 0,
@@ -720,35 +730,34 @@ def rope_table(positions, axis_dims, theta: float = 10000.0, factor: float = 1.0
 
     if positions.dim() != 2 or positions.shape[1] != len(axis_dims):
         raise ValueError(f"positions: expected [T, {len(axis_dims)}], got {tuple(positions.shape)}")
-    _expect(positions, "positions", torch.int32, positions.device)
-    T, axes = positions.shape
+    dev, T = positions.get_device(), positions.shape[0]
+    pos = _expect(positions, "positions", torch.int32, dev)
     if table is None:
         table = torch.empty((T, sum(axis_dims)), dtype=torch.float32, device=positions.device)
-    else:
-        _expect(table, "table", torch.float32, positions.device, (T, sum(axis_dims)))
-    with _on(positions.device):
-        fp4_rope_table(positions, T, axes, axis_dims, theta, factor, window, amplitude, table, stream)
+    _launch(dev, fp4_rope_table, pos, T, len(axis_dims), axis_dims, theta, factor, window, amplitude,
+            _expect(table, "table", torch.float32, dev, (T, sum(axis_dims))), stream)
     return table
 
 
-def _norm_rope_args(q, k, norm, q_weight, k_weight, table):
+def _norm_rope_args(q, k, norm, q_weight, k_weight, eps, table, layout):
+    """The leading arguments of both forms of fp4_qk_norm_rope, after checks."""
     import torch
 
-    q_stride = _expect_rows(q, "q")
+    dev = q.get_device()
+    qp, q_stride = _expect_rows(q, "q", dev)
     T, H_q, D = q.shape
-    k_stride, H_k = 0, 0
+    kp, k_stride, H_k = None, 0, 0
     if k is not None:
-        k_stride, H_k = _expect_rows(k, "k", q.device), k.shape[1]
+        kp, k_stride = _expect_rows(k, "k", dev)
+        H_k = k.shape[1]
         if k.shape[0] != T or k.shape[2] != D:
             raise ValueError(f"k: expected [{T}, heads, {D}], got {tuple(k.shape)}")
     token = _NORM[norm] == NORM_TOKEN
-    _expect(q_weight, "q_weight", torch.float32, q.device, (H_q * D if token else D,))
-    _expect(k_weight, "k_weight", torch.float32, q.device, (H_k * D if token else D,))
-    rot = 0
-    if table is not None:
-        rot = table.shape[-1]
-        _expect(table, "table", torch.float32, q.device, (T, rot))
-    return q_stride, H_q, k_stride, H_k, T, D, rot
+    qw = _expect(q_weight, "q_weight", torch.float32, dev, (H_q * D if token else D,))
+    kw = _expect(k_weight, "k_weight", torch.float32, dev, (H_k * D if token else D,))
+    rot = 0 if table is None else table.shape[-1]
+    tp = _expect(table, "table", torch.float32, dev, (T, rot))
+    return qp, q_stride, H_q, kp, k_stride, H_k, T, D, norm, qw, kw, eps, tp, rot, layout
 
 
 def qk_norm_rope(q, k=None, norm="head", q_weight=None, k_weight=None, eps: float = 1e-6, table=None,
@@ -756,21 +765,19 @@ def qk_norm_rope(q, k=None, norm="head", q_weight=None, k_weight=None, eps: floa
     """RMS norm ("head", "token" or "none") and rotation of bf16 queries [T, H_q, D] and, if given, keys
     [T, H_k, D] in one launch; rows may be slices of a fused projection.  table: fp32 [T, rot] from
     rope_table, or None.  Returns (q_out, k_out), or q_out alone; q_out = q rotates in place."""
-    import torch
-
-    q_stride, H_q, k_stride, H_k, T, D, rot = _norm_rope_args(q, k, norm, q_weight, k_weight, table)
+    args = _norm_rope_args(q, k, norm, q_weight, k_weight, eps, table, layout)
+    dev = q.get_device()
     if q_out is None:
-        q_out = torch.empty((T, H_q, D), dtype=torch.bfloat16, device=q.device)
-    if k is not None and k_out is None:
-        k_out = torch.empty((T, H_k, D), dtype=torch.bfloat16, device=q.device)
-    strides = []
-    for out, x, what in ((q_out, q, "q_out"), (k_out, k, "k_out")):
-        strides.append(_expect_rows(out, what, q.device) if out is not None else 0)
-        if out is not None and (x is None or out.shape != x.shape):
-            raise ValueError(f"{what}: expected the shape of its input, got {tuple(out.shape)}")
-    with _on(q.device):
-        fp4_qk_norm_rope(q, q_stride, H_q, k, k_stride, H_k, T, D, norm, q_weight, k_weight, eps, table, rot, layout,
-                         q_out, strides[0], k_out, strides[1], stream)
+        q_out = q.new_empty(q.shape)
+    if k is None:
+        if k_out is not None:
+            raise ValueError("k_out without k")
+        outs = (*_expect_rows(q_out, "q_out", dev, q.shape), None, 0)
+    else:
+        if k_out is None:
+            k_out = k.new_empty(k.shape)
+        outs = (*_expect_rows(q_out, "q_out", dev, q.shape), *_expect_rows(k_out, "k_out", dev, k.shape))
+    _launch(dev, fp4_qk_norm_rope, *args, *outs, stream)
     return q_out if k is None else (q_out, k_out)
 
 
@@ -781,18 +788,20 @@ def qk_norm_rope_quantize_heads(q, k=None, fmt="mxfp4", norm="head", q_weight=No
     import torch
 
     f = _fmt(fmt)
-    q_stride, H_q, k_stride, H_k, T, D, rot = _norm_rope_args(q, k, norm, q_weight, k_weight, table)
-    _expect(g_q, "g_q", torch.float32, q.device)
-    _expect(g_k, "g_k", torch.float32, q.device)
-    Tpad = (T + 127) // 128 * 128
-    outs = []
-    for H in (H_q, H_k) if k is not None else (H_q,):
-        outs.append((torch.empty((H, Tpad, D // 2), dtype=torch.uint8, device=q.device),
-                     torch.empty((H, fp4_heads_sf_bytes(f, T, H, D) // H), dtype=torch.uint8, device=q.device)))
-    kc, ks = outs[1] if k is not None else (None, None)
-    with _on(q.device):
-        fp4_qk_norm_rope_quantize_heads(f, q, q_stride, H_q, k, k_stride, H_k, T, D, norm, q_weight, k_weight, eps,
-                                        table, rot, layout, g_q, g_k, outs[0][0], outs[0][1], kc, ks, stream)
+    args = _norm_rope_args(q, k, norm, q_weight, k_weight, eps, table, layout)
+    dev, D = q.get_device(), q.shape[2]
+    Tpad = (q.shape[0] + 127) // 128 * 128
+    outs, ptrs = [], []
+    for x in (q,) if k is None else (q, k):
+        H = x.shape[1]
+        codes = torch.empty((H, Tpad, D // 2), dtype=torch.uint8, device=q.device)
+        sf = torch.empty((H, Tpad * (D // (32 if f == MXFP4 else 16))), dtype=torch.uint8, device=q.device)
+        outs.append((codes, sf))
+        ptrs += [codes.data_ptr(), sf.data_ptr()]
+    if k is None:
+        ptrs += [None, None]
+    _launch(dev, fp4_qk_norm_rope_quantize_heads, f, *args, _expect(g_q, "g_q", torch.float32, dev),
+            _expect(g_k, "g_k", torch.float32, dev), *ptrs, stream)
     return outs[0] if k is None else tuple(outs)
 
 
@@ -802,19 +811,16 @@ def dequantize_heads(heads, T: int, fmt="mxfp4", g=None, x=None, stream=None):
 
     f = _fmt(fmt)
     codes, sf = heads
+    dev = codes.get_device()
     H, Tpad, half_d = codes.shape
     if Tpad != (T + 127) // 128 * 128:
         raise ValueError(f"codes of {Tpad} padded tokens do not belong to {T} tokens")
-    _expect(codes, "codes", torch.uint8, codes.device)
-    _expect(sf, "scales", torch.uint8, codes.device, (H, fp4_heads_sf_bytes(f, T, H, 2 * half_d) // H))
-    _expect(g, "g", torch.float32, codes.device)
+    cp = _expect(codes, "codes", torch.uint8, dev)
+    sp = _expect(sf, "scales", torch.uint8, dev, (H, Tpad * (2 * half_d // (32 if f == MXFP4 else 16))))
     if x is None:
         x = torch.empty((T, H, 2 * half_d), dtype=torch.bfloat16, device=codes.device)
-    stride = _expect_rows(x, "x", codes.device)
-    if tuple(x.shape) != (T, H, 2 * half_d):
-        raise ValueError(f"x: expected [{T}, {H}, {2 * half_d}], got {tuple(x.shape)}")
-    with _on(codes.device):
-        fp4_dequantize_heads(f, codes, sf, T, H, 2 * half_d, g, x, stride, stream)
+    _launch(dev, fp4_dequantize_heads, f, cp, sp, T, H, 2 * half_d, _expect(g, "g", torch.float32, dev),
+            *_expect_rows(x, "x", dev, (T, H, 2 * half_d)), stream)
     return x
 
 
@@ -825,26 +831,25 @@ def linear_residual(x, pw: PackedWeight, residual=None, bias=None, act="none", g
     import torch
 
     M, K = x.shape
-    N, dev = pw.N, x.device
+    N, dev = pw.N, x.get_device()
     if K != pw.K:
         raise ValueError(f"x: expected [M, {pw.K}], got {tuple(x.shape)}")
-    _expect(x, "x", torch.bfloat16, dev)
-    _expect(residual, "residual", torch.bfloat16, dev, (M, N))
-    _expect(bias, "bias", torch.float16, dev, (N,))
-    if gate is not None:
-        if gate_rows < 1:
-            raise ValueError("gate_rows: the number of rows of y that share a row of the gate")
-        _expect(gate, "gate", torch.float32, dev, (-(-M // gate_rows), N))
-    _expect(a_global, "a_global", torch.float32, dev)
+    if gate is None:
+        gate_rows = 0
+    elif gate_rows < 1:
+        raise ValueError("gate_rows: the number of rows of y that share a row of the gate")
+    xp = _expect(x, "x", torch.bfloat16, dev)
+    rp = _expect(residual, "residual", torch.bfloat16, dev, (M, N))
+    bp = _expect(bias, "bias", torch.float16, dev, (N,))
+    gp = None if gate is None else _expect(gate, "gate", torch.float32, dev, (-(-M // gate_rows), N))
     if y is None:
-        y = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
-    else:
-        _expect(y, "y", torch.bfloat16, dev, (M, N))
+        y = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
     if workspace is None:
-        workspace = torch.empty(fp4_linear_workspace_bytes(pw.fmt, M, K, N), dtype=torch.uint8, device=dev)
-    with _on(dev):
-        fp4_linear_residual(pw.fmt, x, M, K, N, pw.codes, pw.sf, pw.w_global, a_global, bias, act, gate,
-                            gate_rows if gate is not None else 0, residual, y, workspace, workspace.numel(), stream)
+        workspace = torch.empty(fp4_linear_workspace_bytes(pw.fmt, M, K, N), dtype=torch.uint8, device=x.device)
+    _launch(dev, fp4_linear_residual, pw.fmt, xp, M, K, N, pw.codes, pw.sf, pw.w_global,
+            _expect(a_global, "a_global", torch.float32, dev), bp, act, gp, gate_rows, rp,
+            _expect(y, "y", torch.bfloat16, dev, (M, N)), _expect(workspace, "workspace", torch.uint8, dev),
+            workspace.numel(), stream)
     return y
 
 
@@ -853,14 +858,13 @@ def attn_ranges(q_offsets, k_offsets, T_q: int, T_kv: int, causal=False, prefix=
     offsets [docs + 1], CUDA), in causal order or not, each with a prefix (int32 [docs]) that all its rows see."""
     import torch
 
-    dev, docs = q_offsets.device, q_offsets.numel() - 1
-    _expect(q_offsets, "q_offsets", torch.int32, dev, (docs + 1,))
-    _expect(k_offsets, "k_offsets", torch.int32, dev, (docs + 1,))
-    _expect(prefix, "prefix", torch.int32, dev, (docs,))
-    ranges = torch.empty((2, T_q), dtype=torch.int32, device=dev)
-    with _on(dev):
-        fp4_attn_ranges(q_offsets, k_offsets, docs, T_q, T_kv, causal, prefix, ranges[0], ranges[1], stream)
-    return ranges[0], ranges[1]
+    dev, docs = q_offsets.get_device(), q_offsets.numel() - 1
+    qp = _expect(q_offsets, "q_offsets", torch.int32, dev, (docs + 1,))
+    kp = _expect(k_offsets, "k_offsets", torch.int32, dev, (docs + 1,))
+    pp = _expect(prefix, "prefix", torch.int32, dev, (docs,))
+    start, end = q_offsets.new_empty(T_q), q_offsets.new_empty(T_q)
+    _launch(dev, fp4_attn_ranges, qp, kp, docs, T_q, T_kv, causal, pp, start.data_ptr(), end.data_ptr(), stream)
+    return start, end
 
 
 def attn_bf16(q, k, v, scale: float, softcap: float = 0.0, slopes=None, q_pos: int = 0, key_start=None, key_end=None,
@@ -871,29 +875,27 @@ def attn_bf16(q, k, v, scale: float, softcap: float = 0.0, slopes=None, q_pos: i
     key_start[i] <= j < key_end[i] (int32 [T_q]; None: from the first, to the last)."""
     import torch
 
-    strides = [_expect_rows(t, what, q.device) for t, what in ((q, "q"), (k, "k"), (v, "v"))]
-    dev = q.device
+    dev = q.get_device()
+    qp, q_stride = _expect_rows(q, "q", dev)
     T_q, H, D = q.shape
+    kp, k_stride = _expect_rows(k, "k", dev)
     T_kv, H_kv, _ = k.shape
-    if k.shape != v.shape or k.shape[2] != D:
-        raise ValueError(f"k, v: expected [T_kv, H_kv, {D}], got {tuple(k.shape)}, {tuple(v.shape)}")
-    _expect(slopes, "slopes", torch.float32, dev, (H,))
-    _expect(key_start, "key_start", torch.int32, dev, (T_q,))
-    _expect(key_end, "key_end", torch.int32, dev, (T_q,))
+    if k.shape[2] != D:
+        raise ValueError(f"k: expected [T_kv, H_kv, {D}], got {tuple(k.shape)}")
+    vp, v_stride = _expect_rows(v, "v", dev, k.shape)
     if o is None:
-        o = torch.empty((T_q, H, D), dtype=torch.bfloat16, device=dev)
-    o_stride = _expect_rows(o, "o", dev)
-    if o.shape != q.shape:
-        raise ValueError(f"o: expected {tuple(q.shape)}, got {tuple(o.shape)}")
-    lse = torch.empty((T_q, H), dtype=torch.float32, device=dev) if return_lse else None
+        o = q.new_empty(q.shape)
+    op, o_stride = _expect_rows(o, "o", dev, q.shape)
+    lse = torch.empty((T_q, H), dtype=torch.float32, device=q.device) if return_lse else None
     ws = fp4_attn_bf16_workspace_bytes(T_q, T_kv, H, H_kv, D)
     if workspace is None and ws:
-        workspace = torch.empty(ws, dtype=torch.uint8, device=dev)
-    _expect(workspace, "workspace", torch.uint8, dev)
-    with _on(dev):
-        fp4_attn_bf16(q, strides[0], T_q, k, strides[1], v, strides[2], T_kv, H, H_kv, D, scale, softcap, slopes, q_pos,
-                      key_start, key_end, o, o_stride, lse, workspace, workspace.numel() if workspace is not None else 0,
-                      stream)
+        workspace = torch.empty(ws, dtype=torch.uint8, device=q.device)
+    wp = _expect(workspace, "workspace", torch.uint8, dev)
+    _launch(dev, fp4_attn_bf16, qp, q_stride, T_q, kp, k_stride, vp, v_stride, T_kv, H, H_kv, D, scale, softcap,
+            _expect(slopes, "slopes", torch.float32, dev, (H,)), q_pos,
+            _expect(key_start, "key_start", torch.int32, dev, (T_q,)),
+            _expect(key_end, "key_end", torch.int32, dev, (T_q,)), op, o_stride,
+            None if lse is None else lse.data_ptr(), wp, 0 if workspace is None else workspace.numel(), stream)
     return (o, lse) if return_lse else o
 
 

@@ -54,6 +54,7 @@ struct AttnBfParams {
     bool heads_first;            // item order: key heads fastest, row tiles from the last (masked calls)
     float c;                     // scale log2(e), or (capped) scale / cap
     float cap;                   // capped: cap log2(e)
+    float tanh[6];               //   and the coefficients of tanh_near
     const float* slopes;         // [H] or null
     int64_t q_pos;               // position of query row 0 against key 0 (slopes)
     const int32_t* key_start;    // [T_q] or null (0)
@@ -156,18 +157,17 @@ FP4_DEV void attn_bf_fail(const AttnBfParams& p, volatile int* abort) {
     atomicCAS(p.status, 0, STATUS_TIMEOUT);
 }
 
-// The capped scores of one warp's tile where |x| = |s / cap| <= 1 for all of them: cap log2(e) tanh(x)
-// as an odd polynomial, x P(x^2), fitted here to tanh on [0, 1] (minimax by reweighted least
-// squares, degree 11, within 2^-21), without a transcendental.  c: scale / cap.
-FP4_DEV uint64_t tanh_near(uint64_t s, uint64_t c, uint64_t cap) {
-    const uint64_t x = f2_mul(s, c), y = f2_mul(x, x);
-    uint64_t t = f2_splat(-0x1.742c92p-9f);
-    t = f2_fma(t, y, f2_splat(0x1.0803c2p-6f));
-    t = f2_fma(t, y, f2_splat(-0x1.a191d6p-5f));
-    t = f2_fma(t, y, f2_splat(0x1.0f6ea4p-3f));
-    t = f2_fma(t, y, f2_splat(-0x1.553ce0p-2f));
-    t = f2_fma(t, y, f2_splat(0x1.ffff96p-1f));
-    return f2_mul(f2_mul(x, cap), t);
+// The capped scores of one warp's tile where |s / cap| <= 1 for all of them: cap log2(e) tanh(s / cap)
+// as an odd polynomial s P(s^2), without a transcendental: tanh(x) = x sum_i t_i x^2i fitted here on
+// [0, 1] (minimax by reweighted least squares, degree 11, within 2^-21), the scale and the cap folded
+// into its coefficients on the host.
+constexpr double AB_TANH[6] = {0x1.ffff96p-1, -0x1.553ce0p-2, 0x1.0f6ea4p-3, -0x1.a191d6p-5, 0x1.0803c2p-6, -0x1.742c92p-9};
+FP4_DEV uint64_t tanh_near(uint64_t s, const float (&t)[6]) {
+    const uint64_t y = f2_mul(s, s);
+    uint64_t e = f2_splat(t[5]);
+#pragma unroll
+    for (int i = 4; i >= 0; --i) e = f2_fma(e, y, f2_splat(t[i]));
+    return f2_mul(s, e);
 }
 
 // An item as the planner gives it to the other warps
@@ -541,11 +541,28 @@ __global__ void __launch_bounds__(AB_THREADS, 1)
                 if (!ok) break;
                 tc_fence_after();
                 uint32_t v[4][32];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) tmem_ld_32x32b_x32(t_s + 32 * q, v[q]);
+                tmem_ld_32x32b_x32(t_s, v[0]);
+                tmem_ld_32x32b_x32(t_s + 32, v[1]);
                 tmem_wait_ld();
+                tmem_tie(v[0]);
+                tmem_tie(v[1]);
+                tmem_ld_32x32b_x32(t_s + 64, v[2]);
+                tmem_ld_32x32b_x32(t_s + 96, v[3]);
+                float mx[4];
+                auto row_max = [&](int q) {
+                    float x = __uint_as_float(v[q][0]), y = __uint_as_float(v[q][1]);
 #pragma unroll
-                for (int q = 0; q < 4; ++q) tmem_tie(v[q]);
+                    for (int i = 2; i < 30; i += 4) {
+                        x = fmaxf(fmaxf(x, __uint_as_float(v[q][i])), __uint_as_float(v[q][i + 1]));
+                        y = fmaxf(fmaxf(y, __uint_as_float(v[q][i + 2])), __uint_as_float(v[q][i + 3]));
+                    }
+                    mx[q] = fmaxf(fmaxf(x, y), fmaxf(__uint_as_float(v[q][30]), __uint_as_float(v[q][31])));
+                };
+                // the first half's maximum while the second half is on its way, unless the scores change first
+                if (!CAP && !BIAS) row_max(0), row_max(1);
+                tmem_wait_ld();
+                tmem_tie(v[2]);
+                tmem_tie(v[3]);
                 const int k0 = (jb + (p.alt ? 2 * i + w : i)) * 128;
                 if (CAP) {
                     float far = 0.0f;
@@ -556,13 +573,12 @@ __global__ void __launch_bounds__(AB_THREADS, 1)
                             far = fmaxf(fmaxf(far, fabsf(__uint_as_float(v[q][y]))), fabsf(__uint_as_float(v[q][y + 1])));
                     // (a NaN is passed over by the maximum and stays one in either form)
                     if (__all_sync(0xffffffffu, far * p.c <= 1.0f)) {
-                        const uint64_t c2 = f2_splat(p.c), cap2 = f2_splat(p.cap);
 #pragma unroll
                         for (int q = 0; q < 4; ++q)
 #pragma unroll
                             for (int y = 0; y < 32; y += 2) {
                                 float a, b;
-                                f2_unpack(tanh_near(f2_pack(__uint_as_float(v[q][y]), __uint_as_float(v[q][y + 1])), c2, cap2),
+                                f2_unpack(tanh_near(f2_pack(__uint_as_float(v[q][y]), __uint_as_float(v[q][y + 1])), p.tanh),
                                           a, b);
                                 v[q][y] = __float_as_uint(a), v[q][y + 1] = __float_as_uint(b);
                             }
@@ -590,7 +606,8 @@ __global__ void __launch_bounds__(AB_THREADS, 1)
                 }
                 // the multiplier still to be applied
                 const float c = CAP || BIAS ? 1.0f : p.c;
-                if (k0 < all_lo || k0 + 128 > all_hi) {
+                const bool cut = k0 < all_lo || k0 + 128 > all_hi;
+                if (cut) {
                     const int a = ks - k0, b = ke - k0;
 #pragma unroll
                     for (int q = 0; q < 4; ++q)
@@ -598,15 +615,8 @@ __global__ void __launch_bounds__(AB_THREADS, 1)
                         for (int y = 0; y < 32; ++y)
                             if (32 * q + y < a || 32 * q + y >= b) v[q][y] = 0xFF800000u;
                 }
-                float mx[4];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    mx[q] = __uint_as_float(v[q][0]);
-#pragma unroll
-                    for (int y = 1; y < 31; y += 2)
-                        mx[q] = fmaxf(fmaxf(mx[q], __uint_as_float(v[q][y])), __uint_as_float(v[q][y + 1]));
-                    mx[q] = fmaxf(mx[q], __uint_as_float(v[q][31]));
-                }
+                if (CAP || BIAS || cut) row_max(0), row_max(1);
+                row_max(2), row_max(3);
                 const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
                 const bool grow = top > m + AB_LAZY || (m == -INFINITY && top > m);
                 if (__any_sync(0xffffffffu, grow)) {

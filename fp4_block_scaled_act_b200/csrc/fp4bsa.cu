@@ -1432,7 +1432,8 @@ fp4_status_t fp4_attn_bf16(const void* q_bf16, int64_t q_stride, int64_t T_q, co
                            const int32_t* key_end, void* o_bf16, int64_t o_stride, float* lse, void* workspace,
                            size_t ws_bytes, void* stream) {
     if (!q_bf16 || !k_bf16 || !v_bf16 || !o_bf16) return FP4_ERR_INVALID_ARG;
-    if (!(scale > 0.0f) || !(scale < 1.0e30f) || !(softcap >= 0.0f) || !(softcap < 1.0e30f)) return FP4_ERR_INVALID_ARG;
+    if (!(scale > 0.0f) || !(scale < 1.0e30f) || !(softcap >= 0.0f) || !(softcap <= 1.0e15f * scale))
+        return FP4_ERR_INVALID_ARG;  // (beyond, squares of scores in reach of the cap overflow)
     if (q_pos <= -((int64_t)1 << 40) || q_pos >= ((int64_t)1 << 40)) return FP4_ERR_INVALID_ARG;
     fp4_status_t s = check_attn_bf16(T_q, T_kv, H, H_kv, D);
     if (s != FP4_OK) return s;
@@ -1465,6 +1466,11 @@ fp4_status_t fp4_attn_bf16(const void* q_bf16, int64_t q_stride, int64_t T_q, co
     const double log2e = 1.4426950408889634;
     p.c = (float)(softcap > 0.0f ? (double)scale / softcap : scale * log2e);
     p.cap = (float)(softcap * log2e);
+    if (softcap > 0.0f) {
+        const double x = (double)scale / softcap;  // tanh's argument per unit of q.k
+        double f = softcap * log2e * x;
+        for (int i = 0; i < 6; ++i, f *= x * x) p.tanh[i] = (float)(AB_TANH[i] * f);
+    }
     p.slopes = slopes, p.q_pos = q_pos, p.key_start = key_start, p.key_end = key_end;
     p.v = static_cast<const __nv_bfloat16*>(v_bf16), p.v_stride = v_stride;
     p.o = static_cast<__nv_bfloat16*>(o_bf16), p.o_stride = o_stride, p.lse = lse;
