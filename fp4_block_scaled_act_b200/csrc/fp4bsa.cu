@@ -968,7 +968,7 @@ fp4_status_t check_residual(fp4_fmt_t fmt, int64_t M, int64_t K, int64_t N, cons
     fp4_status_t s = check_shape(M, K, N);
     if (s != FP4_OK) return s;
     if (!aligned16(w_codes) || !aligned16(w_sf) || !aligned16(y_bf16) || !aligned16(bias_f16) || !aligned16(gate) ||
-        (reinterpret_cast<uintptr_t>(residual_bf16) & 31u) || (reinterpret_cast<uintptr_t>(w_global) & 3u) ||
+        !aligned16(residual_bf16) || (reinterpret_cast<uintptr_t>(w_global) & 3u) ||
         (reinterpret_cast<uintptr_t>(a_global) & 3u))
         return FP4_ERR_MISALIGNED;
     return FP4_OK;
@@ -985,8 +985,12 @@ fp4_status_t gemm_residual_impl(fp4_fmt_t fmt, const uint8_t* a_codes, const uin
     if (!aligned16(a_codes) || !aligned16(a_sf)) return FP4_ERR_MISALIGNED;
     DeviceState* ds;
     if ((s = device_state(&ds)) != FP4_OK) return s;
-    // always the 2-CTA kernel
-    CUtensorMap ta, tb;
+    // always the 2-CTA kernel; the residual comes in 32 x 32 boxes, as y leaves
+    CUtensorMap ta, tb, tr;
+    if (residual_bf16 && (s = encode_2d(&tr, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, residual_bf16, (uint64_t)N, (uint64_t)M,
+                                        (uint64_t)N * 2, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B)) != FP4_OK)
+        return s;
+    const CUtensorMap* res = residual_bf16 ? &tr : nullptr;
     if ((s = encode_2d(&ta, CU_TENSOR_MAP_DATA_TYPE_UINT8, a_codes, K / 2, M, K / 2, 128, GEMM_BM)) != FP4_OK)
         return s;
     if ((s = encode_2d(&tb, CU_TENSOR_MAP_DATA_TYPE_UINT8, w_codes, K / 2, N, K / 2, 128, 128)) != FP4_OK) return s;
@@ -1000,8 +1004,8 @@ fp4_status_t gemm_residual_impl(fp4_fmt_t fmt, const uint8_t* a_codes, const uin
     p.res = static_cast<const __nv_bfloat16*>(residual_bf16);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     return fmt == FP4_FMT_NVFP4
-               ? launch_gemm2<G_NVFP4, OUT_RESIDUAL>(ds, ta, tb, a_sf, w_sf, p, st, nullptr, nullptr, pdl)
-               : launch_gemm2<G_MXFP4, OUT_RESIDUAL>(ds, ta, tb, a_sf, w_sf, p, st, nullptr, nullptr, pdl);
+               ? launch_gemm2<G_NVFP4, OUT_RESIDUAL>(ds, ta, tb, a_sf, w_sf, p, st, res, nullptr, pdl)
+               : launch_gemm2<G_MXFP4, OUT_RESIDUAL>(ds, ta, tb, a_sf, w_sf, p, st, res, nullptr, pdl);
 }
 }  // namespace
 

@@ -136,72 +136,77 @@ FP4_DEV void epilogue_store(const GemmParams& p, uint32_t (&acc)[NC][32], int ro
                 make_uint4(acc[c][4 * g], acc[c][4 * g + 1], acc[c][4 * g + 2], acc[c][4 * g + 3]);
 }
 
-// Gated residual epilogue: 64 columns of one row, as epilogue_pack, but
+// Gated residual epilogue: 8 columns of one row,
 //   y = bf16_rn(res + gate * act(acc gs + bias))
 // with everything after the accumulator in fp32 and one rounding (gate * act + res is one fma).
-// res: the row's 64 residual values, loaded ahead (ld_residual).
-FP4_DEV void act_x2(int act, float& a, float& b) {
-    if (act == 1) {
-        gelu_f32_x2(a, b, a, b);
-    } else if (act == 2) {  // z / (1 + exp(-z)); exp overflows to infinity, whose reciprocal is 0
-        a *= __frcp_rn(1.0f + exp2f(a * -1.44269504f));
-        b *= __frcp_rn(1.0f + exp2f(b * -1.44269504f));
-    }
+// Both activations are z / (1 + 2^t): SiLU with t = -z log2 e, GELU-tanh with t = -2 sqrt(2/pi) (z +
+// 0.044715 z^3) log2 e.  2^t and the reciprocal are the hardware's approximations, together within
+// 5 2^-23 relative; 2^t overflows to infinity, whose reciprocal gives a zero of z's sign.  The exact
+// GELU of gelu.cuh and exp2f with a rounded reciprocal cost 330 and 945 us at 75600 x 5120 x 5120.
+FP4_DEV float act_of(int act, float z) {
+    if (act == 0) return z;
+    const float w = act == 1 ? __fmaf_rn(z * z * 0.044715f, z, z) : z;
+    const float t = w * (act == 1 ? -2.30220819f : -1.44269504f);
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+    return z * r;
 }
-FP4_DEV void ld_residual(const GemmParams& p, int row, int col0, uint32_t (&res)[4][8]) {
-    if (p.res && row < p.M && col0 < p.N) {
+// Row r of a 32 x 32 chunk at column col0, in a tile with 64-byte rows under the 64-byte swizzle (as
+// epilogue_stage_32): the residual, brought there by TMA, is read from it and the result, stored by TMA,
+// written over it.  Beside the operand stream a tile comes back only some 2000 cycles after its store was
+// issued and a load takes as long, so each warp has three tiles for its four chunks: with two the
+// call took 1.3 times as long.  Neither way past TMA is open: row by row from the lanes that hold
+// them, loads stretched the epilogue by 4 us a tile, and a transpose through shared memory (which the
+// operands saturate) with plain loads and stores by 12 us.
+template <int ACT>
+FP4_DEV void residual_chunk(const GemmParams& p, const uint32_t (&acc)[32], uint8_t* tile, int r, const float* gate,
+                            int col0, float gs) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) ld_global_v8(p.res + (size_t)row * p.N + col0 + 16 * i, res[i]);
-    }
-}
-FP4_DEV void epilogue_pack_residual(const GemmParams& p, uint32_t (&acc)[2][32], const uint32_t (&res)[4][8], int row,
-                                    int col0, float gs) {
-    const float* gate = p.gate ? p.gate + (size_t)(row / p.gate_rows) * p.N + col0 : nullptr;
+    for (int j = 0; j < 4; ++j) {
+        uint4* at = reinterpret_cast<uint4*>(tile + r * 64 + ((j ^ (r >> 1)) & 3) * 16);
+        const int col = col0 + 8 * j;
+        float v[8];
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-#pragma unroll
-        for (int j = 0; j < 32; j += 8) {
-            float v[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = __fmul_rn(__uint_as_float(acc[c][j + i]), gs);
-            if (p.bias) {
-                const uint4 bv = __ldg(reinterpret_cast<const uint4*>(p.bias + col0 + c * 32 + j));
-                const __half2* bh = reinterpret_cast<const __half2*>(&bv);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float2 bf = __half22float2(bh[i]);
-                    v[2 * i] = __fmaf_rn(__uint_as_float(acc[c][j + 2 * i]), gs, bf.x);
-                    v[2 * i + 1] = __fmaf_rn(__uint_as_float(acc[c][j + 2 * i + 1]), gs, bf.y);
-                }
-            }
-            if (p.act) {
-#pragma unroll
-                for (int i = 0; i < 8; i += 2) act_x2(p.act, v[i], v[i + 1]);
-            }
-            float g[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) g[i] = 1.0f;
-            if (gate) {
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const float4 f = __ldg(reinterpret_cast<const float4*>(gate + c * 32 + j + 4 * i));
-                    g[4 * i] = f.x, g[4 * i + 1] = f.y, g[4 * i + 2] = f.z, g[4 * i + 3] = f.w;
-                }
-            }
+        for (int i = 0; i < 8; ++i) v[i] = __fmul_rn(__uint_as_float(acc[8 * j + i]), gs);
+        if (p.bias) {
+            const uint4 bv = __ldg(reinterpret_cast<const uint4*>(p.bias + col));
+            const __half2* bh = reinterpret_cast<const __half2*>(&bv);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const uint32_t w = res[(c * 32 + j) / 16][(j % 16) / 2 + i];
-                float lo, hi;
-                if (p.res) {
-                    lo = __fmaf_rn(g[2 * i], v[2 * i], __uint_as_float(w << 16));
-                    hi = __fmaf_rn(g[2 * i + 1], v[2 * i + 1], __uint_as_float(w & 0xFFFF0000u));
-                } else {
-                    lo = g[2 * i] * v[2 * i], hi = g[2 * i + 1] * v[2 * i + 1];
-                }
-                const __nv_bfloat162 b2 = __floats2bfloat162_rn(lo, hi);
-                acc[c][j / 2 + i] = *reinterpret_cast<const uint32_t*>(&b2);
+                const float2 bf = __half22float2(bh[i]);
+                v[2 * i] = __fmaf_rn(__uint_as_float(acc[8 * j + 2 * i]), gs, bf.x);
+                v[2 * i + 1] = __fmaf_rn(__uint_as_float(acc[8 * j + 2 * i + 1]), gs, bf.y);
             }
         }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = act_of(ACT, v[i]);
+        float g[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) g[i] = 1.0f;
+        if (gate) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float4 f = __ldg(reinterpret_cast<const float4*>(gate + col + 4 * i));
+                g[4 * i] = f.x, g[4 * i + 1] = f.y, g[4 * i + 2] = f.z, g[4 * i + 3] = f.w;
+            }
+        }
+        const uint4 res = p.res ? *at : make_uint4(0u, 0u, 0u, 0u);
+        const uint32_t rw[4] = {res.x, res.y, res.z, res.w};
+        uint32_t out[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float lo, hi;
+            if (p.res) {
+                lo = __fmaf_rn(g[2 * i], v[2 * i], __uint_as_float(rw[i] << 16));
+                hi = __fmaf_rn(g[2 * i + 1], v[2 * i + 1], __uint_as_float(rw[i] & 0xFFFF0000u));
+            } else {
+                lo = g[2 * i] * v[2 * i], hi = g[2 * i + 1] * v[2 * i + 1];
+            }
+            const __nv_bfloat162 b2 = __floats2bfloat162_rn(lo, hi);
+            out[i] = *reinterpret_cast<const uint32_t*>(&b2);
+        }
+        *at = make_uint4(out[0], out[1], out[2], out[3]);
     }
 }
 
@@ -520,10 +525,12 @@ struct Gemm2Cfg {
     // operand producer loads them with the stage's tiles (SC_STAGES == STAGES, slot s of the
     // scale area belongs to operand stage s and is recycled with it).
     static constexpr bool SEP_SC = (KIND != G_NVFP4);
-    static constexpr int STAGES = (KIND == G_W4A8) ? 6 : 5;
+    // (the gated residual output, OUTQ 3, has larger staging tiles; beside NVFP4's scales they cost a stage)
+    static constexpr bool RESIDUAL = OUTQ == 3;
+    static constexpr int STAGES = (KIND == G_W4A8) ? 6 : (RESIDUAL && KIND == G_NVFP4) ? 4 : 5;
     static constexpr int SC_STAGES = SEP_SC ? 4 : STAGES;
-    static constexpr int EPI_COLS = (STAGES == 6) ? 32 : 64;
-    static constexpr int EPI_TILE = 32 * EPI_COLS * 2;
+    static constexpr int EPI_COLS = (STAGES == 6 || RESIDUAL) ? 32 : 64;
+    static constexpr int EPI_TILE = 32 * EPI_COLS * 2 * (RESIDUAL ? 3 : 1);  // three tiles a warp (residual_chunk)
     static constexpr int EPI_BYTES = 8 * EPI_TILE;
     // the dynamic shared array is declared 1024-byte aligned (checked at run time), so the
     // layout needs no alignment slack
@@ -544,10 +551,10 @@ struct Gemm2Cfg {
     // refill a buffer four stages after its MMAs were issued rather than two.  The fused
     // GELU epilogues keep a 64-column overlap (their holders convert before releasing it)
     // and two buffers; W4A8 (one atom, 12 columns) fits four buffers beside a 64 overlap.
-    static constexpr int ACC1_COL = (KIND == G_NVFP4) ? 160 : (KIND == G_W4A8 || OUTQ != 0) ? 192 : 160;
+    static constexpr int ACC1_COL = (KIND == G_NVFP4) ? 160 : (KIND == G_W4A8 || (OUTQ != 0 && !RESIDUAL)) ? 192 : 160;
     static constexpr int SF_COL0 = ACC1_COL + 256;
     static constexpr int OVL = 256 - ACC1_COL;
-    static constexpr bool HOLD_ALL = (OUTQ == 0) && (OVL > 64);
+    static constexpr bool HOLD_ALL = (OUTQ == 0 || RESIDUAL) && (OVL > 64);
     static constexpr int SFA_COLS = 4 * ATOMS;        // A: 4 columns per atom
     static constexpr int SF_COLS = SFA_COLS + 8 * ATOMS;  // B: 8 columns per atom
     static constexpr int TB = ((GEMM_TMEM_COLS - SF_COL0) / SF_COLS) >= 4 ? 4 : ((GEMM_TMEM_COLS - SF_COL0) / SF_COLS);
@@ -721,7 +728,7 @@ FP4_DEV void arrive_leader_relaxed(uint64_t* bar, uint32_t rank) {
 
 // OUTQ 0: bf16 output through the TMA-store epilogue; 1 / 2: the fused GELU + MXFP4 /
 // NVFP4 quantize epilogue (epilogue_gelu_quant) in place of the bf16 output; OUT_RESIDUAL:
-// bf16 output through activation, gate and residual (epilogue_pack_residual).
+// bf16 output through activation, gate and residual (residual_chunk; tmU is the residual's map).
 // SK: the stream-K schedule (small problems, opt-in); a separate instantiation so the
 // default kernel carries none of its registers.
 template <int KIND, int OUTQ = 0, bool SK = false>
@@ -761,7 +768,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Gemm2Cfg<KIND>::THRE
     uint64_t* acc_free = tmem_full + 2;                   // [2]
     uint64_t* ovl_free = acc_free + 2;
     uint64_t* mma_done = ovl_free + 1;
-    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(mma_done + 1);
+    uint64_t* res_full = mma_done + 1;                    // [8 epilogue warps][3] residual tile loaded (RESIDUAL)
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(res_full + 24);
     volatile int* abort = reinterpret_cast<volatile int*>(tmem_holder + 1);
 
     const int warp = threadIdx.x >> 5;
@@ -785,6 +793,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Gemm2Cfg<KIND>::THRE
         }
         mbar_init(ovl_free, 8);
         mbar_init(mma_done, 1);
+        for (int i = 0; i < 24; ++i) mbar_init(&res_full[i], 1);
         *abort = 0;
         fence_mbar_init();
     }
@@ -853,6 +862,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Gemm2Cfg<KIND>::THRE
             named_bar_sync(EPI_TABLE_BAR, 256u);
         }
         int tcount = 0;
+        [[maybe_unused]] uint32_t res_tiles = 0;  // output tiles with a residual so far
         Sched sc = sched0;
         sc.begin();
         int tile, kb0, kb1;
@@ -866,11 +876,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Gemm2Cfg<KIND>::THRE
             const bool holds_overlap = (h == (b == 0 ? 1 : 0));
             const int first = holds_overlap ? (b == 0 ? 2 : 0) : 0;
             const int second = 2 - first;
-            [[maybe_unused]] uint32_t res[4][8];  // residual values of the half drained next
-            if (OUTQ == OUT_RESIDUAL) ld_residual(p, row, col0 + first * 32, res);
+            // gated residual: chunk k of the four, in the order of draining, goes through tile k % 3; the first
+            // three residual chunks are on their way before the accumulator is complete
+            const bool with_res = C::RESIDUAL && p.res && col0 < p.N && row0 < p.M;
+            auto load_res = [&](int k) {  // (lane 0)
+                uint64_t* bar = &res_full[3 * ew + k % 3];
+                mbar_arrive_expect_tx(bar, 2048);
+                tma_load_2d(stile + (k % 3) * 2048, &tmU, bar, col0 + ((k < 2 ? first : second) + (k & 1)) * 32, row0, pol_y);
+            };
+            if (with_res && lane == 0) {
+                bulk_wait_group_read0();
+                for (int k = 0; k < 3; ++k) load_res(k);
+            }
             const bool got = mbar_wait(&tmem_full[b], ((uint32_t)tcount >> 1) & 1u, p.timeout_ns, abort);
             if (!__all_sync(0xffffffffu, got)) {
-                if (lane == 0) gemm2_fail(p, abort, peer_abort);
+                if (lane == 0) {
+                    gemm2_fail(p, abort, peer_abort);
+                    // copies in flight must land before the CTA exits
+                    for (int k = 0; with_res && k < 3; ++k)
+                        mbar_wait_drain(&res_full[3 * ew + k], k == 0 ? 0u : res_tiles & 1u, p.timeout_ns);
+                }
                 break;
             }
             tc_fence_after();
@@ -896,16 +921,54 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Gemm2Cfg<KIND>::THRE
                     return;
                 }
                 if (col0 >= p.N) return;
-                if constexpr (C::EPI_COLS == 64) {
-                    if constexpr (OUTQ == OUT_RESIDUAL) {
-                        if (row < p.M) epilogue_pack_residual(p, a, res, row, col0 + chunk * 32, gs);
-                        // the other half's residual is on its way while this half is stored
-                        if (chunk == first) ld_residual(p, row, col0 + second * 32, res);
+                if constexpr (C::RESIDUAL) {
+                    if (row0 >= p.M) return;
+                    const float* gate =
+                        p.gate ? p.gate + (size_t)((row < p.M ? row : p.M - 1) / p.gate_rows) * p.N : nullptr;
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const int k = (chunk == first ? 0 : 2) + c, col = col0 + (chunk + c) * 32;
+                        uint8_t* tile = stile + (k % 3) * 2048;
+                        if (with_res) {
+                            // tile 0 is loaded twice for every output tile, tiles 1 and 2 once
+                            const uint32_t parity = k % 3 == 0 ? (k == 3 ? 1u : 0u) : res_tiles & 1u;
+                            const bool loaded = mbar_wait(&res_full[3 * ew + k % 3], parity, p.timeout_ns, abort);
+                            if (!__all_sync(0xffffffffu, loaded) && lane == 0) gemm2_fail(p, abort, peer_abort);
+                        } else {
+                            // the last store from this tile: the newest for chunk 0 (the chunk 3 before), else
+                            // three back at least
+                            if (lane == 0) {
+                                if (k == 0)
+                                    bulk_wait_group_read0();
+                                else
+                                    bulk_wait_group_read2();
+                            }
+                            __syncwarp();
+                        }
+                        if (p.act == 0)
+                            residual_chunk<0>(p, a[c], tile, lane, gate, col, gs);
+                        else if (p.act == 1)
+                            residual_chunk<1>(p, a[c], tile, lane, gate, col, gs);
+                        else
+                            residual_chunk<2>(p, a[c], tile, lane, gate, col, gs);
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            tma_store_2d_hint(&tmY, tile, col, row0, pol_y);
+                            bulk_commit_group();
+                            if (with_res && k == 1) {  // chunk 0's store has had chunk 1's time to be read
+                                bulk_wait_group_read1();
+                                load_res(3);
+                            }
+                        }
+                        __syncwarp();
+                        if (with_res && k == 3) ++res_tiles;
                     }
+                } else if constexpr (C::EPI_COLS == 64) {
                     if (lane == 0) bulk_wait_group_read0();
                     __syncwarp();
                     if (row < p.M) {
-                        if constexpr (OUTQ == 0) epilogue_pack<KIND, 2>(p, a, row, col0 + chunk * 32, gs);
+                        epilogue_pack<KIND, 2>(p, a, row, col0 + chunk * 32, gs);
                         epilogue_stage_64(a, stile, lane);
                     }
                     fence_proxy_async_smem();
@@ -1230,7 +1293,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Gemm2Cfg<KIND>::THRE
                     const uint32_t dacc = tmem_base + (uint32_t)(b * C::ACC1_COL);
                     for (int kb = kb0; kb < kb1 + (HAS_LR ? 1 : 0); ++kb, ++it) {
                         named_bar_sync(1u + (uint32_t)t, 64u);
-                        if (lane == 0 && HAS_LR && kb == num_kb) {
+                        if constexpr (C::RESIDUAL) {
+                            // issued from converged code: this epilogue keeps the SM busy (mma2x4_...)
+                            tc_fence_after();
+                            const uint64_t adesc = adesc0 + (uint64_t)(s * (C::A_BYTES >> 4));
+                            const uint64_t bdesc = bdesc0 + (uint64_t)(s * (C::B_BYTES >> 4));
+                            const uint32_t tsfa = tmem_base + C::SF_COL0 + (uint32_t)(t * C::SF_COLS);
+                            const uint32_t four = K - kb * C::BK < C::BK ? 0u : 1u, acc0 = kb > kb0 ? 1u : 0u;
+                            if constexpr (KIND == G_NVFP4)
+                                mma2x4_mxf4nvf4_block16(dacc, adesc, bdesc, C::IDESC, acc0, tsfa, tsfa + C::SFA_COLS, four);
+                            else
+                                mma2x4_mxf4nvf4_block32(dacc, adesc, bdesc, C::IDESC, acc0, tsfa, tsfa + C::SFA_COLS, four);
+                            tc_commit_pair_elect(&empty[s], 0x3);
+                        } else if (lane == 0 && HAS_LR && kb == num_kb) {
                             // low-rank stage: acc += u_hi L2 + u_lo L2 (bf16 x bf16 -> fp32)
                             tc_fence_after();
                             const uint32_t a_base = smem_u32(sA + s * C::A_BYTES);
@@ -1276,12 +1351,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Gemm2Cfg<KIND>::THRE
                         if (++s == S) s = 0;
                         if (++t == TB) t = 0;
                     }
-                    if (lane == 0) tc_commit_pair(&tmem_full[b], 0x3);
+                    if constexpr (C::RESIDUAL)
+                        tc_commit_pair_elect(&tmem_full[b], 0x3);
+                    else if (lane == 0)
+                        tc_commit_pair(&tmem_full[b], 0x3);
                     __syncwarp();
                     if (__any_sync(0xffffffffu, *abort != 0)) ok = false;
                 }
                 if (issued) {
-                    if (lane == 0) tc_commit_pair(mma_done, 0x1);
+                    if constexpr (C::RESIDUAL)
+                        tc_commit_pair_elect(mma_done, 0x1);
+                    else if (lane == 0)
+                        tc_commit_pair(mma_done, 0x1);
                     __syncwarp();
                     const bool drained = mbar_wait_drain(mma_done, 0, p.timeout_ns);
                     if (!__all_sync(0xffffffffu, drained) && lane == 0) gemm2_fail(p, abort, peer_abort);

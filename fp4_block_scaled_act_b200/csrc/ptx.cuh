@@ -160,6 +160,9 @@ FP4_DEV void tma_store_2d_hint(const CUtensorMap* map, const void* src, int x, i
 }
 FP4_DEV void bulk_commit_group() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 FP4_DEV void bulk_wait_group_read0() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+// (all but the newest one or two groups)
+FP4_DEV void bulk_wait_group_read1() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
+FP4_DEV void bulk_wait_group_read2() { asm volatile("cp.async.bulk.wait_group.read 2;" ::: "memory"); }
 FP4_DEV void bulk_wait_group0() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 FP4_DEV void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
@@ -303,15 +306,8 @@ FP4_DEV void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t (&v)[16]) {
 }
 FP4_DEV void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// ------------------------------------------------------------------ plain loads
+// ------------------------------------------------------------------ plain stores
 // 32 bytes per thread (32-byte aligned): one whole sector a lane.
-FP4_DEV void ld_global_v8(const void* p, uint32_t (&r)[8]) {
-    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-                 : "l"(p)
-                 : "memory");
-}
-
 FP4_DEV void st_global_v8(void* p, const uint32_t (&r)[8]) {
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]),
                  "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
@@ -444,6 +440,51 @@ FP4_DEV void mma2_mxf8f6f4_block32(uint32_t d, uint64_t a, uint64_t b, uint32_t 
         "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(sfa), "r"(sfb)
         : "memory");
 }
+// The four MMAs of a 256-wide FP4 stage (32 bytes of every operand row each) issued by one elected lane
+// of a converged warp with warp-uniform operands, which then stay in uniform registers: beside a busy
+// epilogue an MMA from a single lane's branch takes more than twice as long to issue.  block32: MMA k
+// reads scale bytes 2 (k % 2), +1 of atom k / 2; block16: the whole word of atom k.  A stage of 128
+// elements (`four` = 0) has the first two only.
+FP4_DEV void mma2x4_mxf4nvf4_block32(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc, uint32_t sfa,
+                                     uint32_t sfb, uint32_t four) {
+    asm volatile(
+        "{\n\t.reg .pred e, f, p;\n\t.reg .b64 x, y;\n\t.reg .b32 i, u, v;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.and.b32 f, %7, 0, e;\n\tsetp.ne.b32 p, %4, 0;\n\tor.b32 i, %3, 0x40000020;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.block32 [%0], %1, %2, %3, [%5], [%6], p;\n\t"
+        "setp.eq.b32 p, 0, 0;\n\tadd.s64 x, %1, 2;\n\tadd.s64 y, %2, 2;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.block32 [%0], x, y, i, [%5], [%6], p;\n\t"
+        "add.s64 x, %1, 4;\n\tadd.s64 y, %2, 4;\n\tadd.s32 u, %5, 4;\n\tadd.s32 v, %6, 8;\n\t"
+        "@f tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.block32 [%0], x, y, %3, [u], [v], p;\n\t"
+        "add.s64 x, %1, 6;\n\tadd.s64 y, %2, 6;\n\t"
+        "@f tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.block32 [%0], x, y, i, [u], [v], p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(sfa), "r"(sfb), "r"(four)
+        : "memory");
+}
+FP4_DEV void mma2x4_mxf4nvf4_block16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc, uint32_t sfa,
+                                     uint32_t sfb, uint32_t four) {
+    asm volatile(
+        "{\n\t.reg .pred e, f, p;\n\t.reg .b64 x, y;\n\t.reg .b32 u, v;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.and.b32 f, %7, 0, e;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.block16 [%0], %1, %2, %3, [%5], [%6], p;\n\t"
+        "setp.eq.b32 p, 0, 0;\n\tadd.s64 x, %1, 2;\n\tadd.s64 y, %2, 2;\n\tadd.s32 u, %5, 4;\n\tadd.s32 v, %6, 8;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.block16 [%0], x, y, %3, [u], [v], p;\n\t"
+        "add.s64 x, %1, 4;\n\tadd.s64 y, %2, 4;\n\tadd.s32 u, %5, 8;\n\tadd.s32 v, %6, 16;\n\t"
+        "@f tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.block16 [%0], x, y, %3, [u], [v], p;\n\t"
+        "add.s64 x, %1, 6;\n\tadd.s64 y, %2, 6;\n\tadd.s32 u, %5, 12;\n\tadd.s32 v, %6, 24;\n\t"
+        "@f tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.block16 [%0], x, y, %3, [u], [v], p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(sfa), "r"(sfb), "r"(four)
+        : "memory");
+}
+// tc_commit_pair by the lane that issues those groups
+FP4_DEV void tc_commit_pair_elect(uint64_t* bar, uint16_t cta_mask) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(
+            smem_u32(bar)),
+        "h"(cta_mask)
+        : "memory");
+}
+
 // Dense bf16 x bf16 -> fp32 MMA of the pair (kind::f16, K = 16 per instruction).
 FP4_DEV void mma2_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
     asm volatile(

@@ -241,8 +241,9 @@ fp4_status_t fp4_linear_gelu_quant(fp4_fmt_t fmt, const void* x_bf16, int64_t M,
 
 typedef enum {
     FP4_ACT_NONE = 0,
-    FP4_ACT_GELU_TANH = 1, /* evaluated in fp32 as described above, not rounded to bf16 */
+    FP4_ACT_GELU_TANH = 1, /* as above, not rounded to bf16 */
     FP4_ACT_SILU = 2       /* z / (1 + exp(-z)) */
+    /* both evaluated in fp32 as z / (1 + 2^t) within (2 |t| + 8) 2^-23 of their value and 2^-126 */
 } fp4_act_t;
 
 /* A block's output projection with what follows it (Wan2.2 blocks: x + proj(h) * gate, the gate
@@ -252,7 +253,7 @@ typedef enum {
  *   act            activation
  *   gate           (device) fp32 [ceil(M / gate_rows)][N]: one row for gate_rows rows of y (a
  *                  clip's tokens; 1: a gate per token), or NULL with gate_rows = 0 (a gate of 1)
- *   residual_bf16  (device) [M, N] bf16, 32-byte aligned, or NULL (0); y_bf16 may be the same
+ *   residual_bf16  (device) [M, N] bf16, or NULL (0); y_bf16 may be the same
  *                  memory (not any other overlap)
  * Other arguments as fp4_gemm.  Always the 2-CTA kernel. */
 fp4_status_t fp4_gemm_residual(fp4_fmt_t fmt, const uint8_t* a_codes, const uint8_t* a_sf, int64_t M, int64_t K,

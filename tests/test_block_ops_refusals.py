@@ -93,7 +93,7 @@ RESIDUAL = [
     (INVALID, dict(fmt=2)), (INVALID, dict(w_codes=None)), (INVALID, dict(w_sf=None)), (INVALID, dict(y=None)),
     (INVALID, dict(w_global=A)), (INVALID, dict(fmt=1)), (INVALID, dict(fmt=1, w_global=A)), (INVALID, dict(act=3)),
     (INVALID, dict(gate_rows=0)), (INVALID, dict(gate=None)), (INVALID, dict(M=0)), (SHAPE, dict(K=200)),
-    (SHAPE, dict(N=192)), (SHAPE, dict(M=1 << 30)), (MISALIGNED, dict(residual=A + 16)), (MISALIGNED, dict(y=BAD)),
+    (SHAPE, dict(N=192)), (SHAPE, dict(M=1 << 30)), (MISALIGNED, dict(residual=BAD)), (MISALIGNED, dict(y=BAD)),
     (MISALIGNED, dict(gate=A + 4)), (MISALIGNED, dict(bias=A + 2)), (MISALIGNED, dict(w_sf=BAD))]
 
 
