@@ -92,28 +92,49 @@ FP4_DEV uint32_t bf16_pack(float lo, float hi) {
 }
 FP4_DEV float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 FP4_DEV float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+// Larger magnitudes of two pairs of bf16 (the signs become the exclusive or of both); a NaN
+// beside a number drops out.
+FP4_DEV uint32_t bf16_absmax2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("max.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
 
-// A pair (u, v) rotated in fp32, to bf16 by both ends of its error.  In fp32 a = x0 (w0 r) carries
-// three roundings and so does b; u = a c - b s carries two more, so u is within
+// Two pairs (u, v) rotated in fp32, to bf16 by both ends of their errors.  In fp32
+// a = x0 w0 carries one rounding (where it is no subnormal) and so does b, c r and s r carry two;
+// u = a (c r) - b (s r) carries two more, so u is, with r in c and s, within
 // 2^-24 (3 (|a c| + |b s|) + |b s| + |u|) of the exact value, where |a c| + |b s| <= sqrt(u^2 + v^2)
 // since (c, s) is a scaled rotation: with t = max(|u|, |v|) at most 2^-24 (4 sqrt(2) t + |u|).
 // m = 2^-21 t covers that and the rounding of u - m and u + m (2^-24 |u|); the same holds for v.
-// Where both round to the same bf16 that is the answer; elsewhere (some 3 in 10,000 values) the
-// pair is taken again in fp64 (rot_exact).  Unrotated values have the bound of a alone.
-FP4_DEV uint32_t low_high(float u, float v, uint32_t& high) {
-    const float t = fmaxf(fabsf(u), fabsf(v));
-    const uint64_t uv = f2_pack(u, v), tt = f2_pack(t, t);
-    float a, b;
-    f2_unpack(f2_fma(tt, f2_splat(0x1p-21f), uv), a, b);
-    high = bf16_pack(a, b);
-    f2_unpack(f2_fma(tt, f2_splat(-0x1p-21f), uv), a, b);
-    return bf16_pack(a, b);
+// Where both round to the same bf16 that is the answer; elsewhere (some 2 in 1000 pairs) the pair is
+// taken again in fp64 (rot_exact).  Unrotated values have the bound of a alone.
+// SIDE: the words are (u, u') and (v, v'), else (u, v) and (u', v'); bit 0 / 1 of
+// the result: the first / second pair differs.
+template <bool SIDE>
+FP4_DEV uint32_t low_high(uint64_t u2, uint64_t v2, uint32_t& w0, uint32_t& w1) {
+    float u[2], v[2], lu[2], lv[2], hu[2], hv[2];
+    f2_unpack(u2, u[0], u[1]);
+    f2_unpack(v2, v[0], v[1]);
+    const uint64_t t = f2_pack(fmaxf(fabsf(u[0]), fabsf(v[0])), fmaxf(fabsf(u[1]), fabsf(v[1])));
+    f2_unpack(f2_fma(t, f2_splat(-0x1p-21f), u2), lu[0], lu[1]);
+    f2_unpack(f2_fma(t, f2_splat(-0x1p-21f), v2), lv[0], lv[1]);
+    f2_unpack(f2_fma(t, f2_splat(0x1p-21f), u2), hu[0], hu[1]);
+    f2_unpack(f2_fma(t, f2_splat(0x1p-21f), v2), hv[0], hv[1]);
+    w0 = SIDE ? bf16_pack(lu[0], lu[1]) : bf16_pack(lu[0], lv[0]);
+    w1 = SIDE ? bf16_pack(lv[0], lv[1]) : bf16_pack(lu[1], lv[1]);
+    const uint32_t h0 = SIDE ? bf16_pack(hu[0], hu[1]) : bf16_pack(hu[0], hv[0]);
+    const uint32_t h1 = SIDE ? bf16_pack(hv[0], hv[1]) : bf16_pack(hu[1], hv[1]);
+    if (SIDE) {
+        const uint32_t d = (w0 ^ h0) | (w1 ^ h1);
+        return ((d & 0xFFFFu) ? 1u : 0u) | ((d >> 16) ? 2u : 0u);
+    }
+    return (w0 != h0 ? 1u : 0u) | (w1 != h1 ? 2u : 0u);
 }
-// The same pair in fp64: (u, v) as two bf16 in one word.  (c, s) = (1, 0) leaves it unrotated.
-FP4_DEV uint32_t rot_exact(float x0, float x1, float w0, float w1, double r, float c, float s) {
+// The same pair in fp64: (u, v) as two bf16 in one word.
+FP4_DEV uint32_t rot_exact(float x0, float x1, float w0, float w1, double r, bool turned, float c, float s) {
     const double a = (double)x0 * (double)w0, b = (double)x1 * (double)w1;
-    const double u = s == 0.0f ? a * (double)c : a * (double)c - b * (double)s;
-    const double v = s == 0.0f ? b * (double)c : a * (double)s + b * (double)c;
+    double u = a, v = b;
+    if (turned) u = a * (double)c - b * (double)s, v = a * (double)s + b * (double)c;
     return bf16_bits_exact(u * r) | bf16_bits_exact(v * r) << 16;
 }
 
@@ -166,34 +187,41 @@ __global__ void __launch_bounds__(NR_THREADS, 5)
             cp_async_16(mine_at + i * 64 + 32, src + e1);
         }
     }
-    float six_g = 6.0f;
+    float six_g = 6.0f, per_six_g = 0.0f;
     if (OUT == NR_NVFP4) {
         // 1 / (e4m3(sf) g) for every scale byte, by the activation quantizer's operations
         const float g = *q.g;
         six_g = __fmul_rn(6.0f, g);
+        per_six_g = six_g >= 0x1p-100f && six_g <= 0x1p100f ? __frcp_rn(six_g) : 0.0f;
         const float d = __fmul_rn(e4m3_to_f32(threadIdx.x), g);
         nv_rcp[threadIdx.x] = d == 0.0f ? 0.0f : __frcp_rn(d);
         __syncthreads();
     }
     const float* const row = p.table + t * p.rot;
-    float cs[16];  // eight (cos, sin) pairs
+    // its eight pairs' cosines and sines, two pairs to a word pair
+    uint64_t cs[4], sn[4];
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
         float4 f = make_float4(1.0f, 0.0f, 1.0f, 0.0f);
         if (real && (c < 2 ? turned0 : turned1))
             f = __ldg(reinterpret_cast<const float4*>(row + (c < 2 ? c0 : c1 - 8) + 4 * c));
-        cs[4 * c] = f.x, cs[4 * c + 1] = f.y, cs[4 * c + 2] = f.z, cs[4 * c + 3] = f.w;
+        cs[c] = f2_pack(f.x, f.z), sn[c] = f2_pack(f.y, f.w);
     }
     cp_async_wait_all();
-    // a unit's sum of squares: four squares at a time in fp32, the rest in fp64
+    // a unit's sum of squares: eight squares at a time in fp32, the rest in fp64
     auto squares = [](const uint32_t (&x)[8]) {
         double sum = 0.0;
 #pragma unroll
-        for (int k = 0; k < 8; k += 2) {
-            const uint64_t a = f2_pack(bf16_lo(x[k]), bf16_hi(x[k]));
-            const uint64_t b = f2_pack(bf16_lo(x[k + 1]), bf16_hi(x[k + 1]));
+        for (int k = 0; k < 8; k += 4) {
+            uint64_t s = f2_pack(bf16_lo(x[k]), bf16_hi(x[k]));
+            s = f2_mul(s, s);
+#pragma unroll
+            for (int e = 1; e < 4; ++e) {
+                const uint64_t a = f2_pack(bf16_lo(x[k + e]), bf16_hi(x[k + e]));
+                s = f2_fma(a, a, s);
+            }
             float s0, s1;
-            f2_unpack(f2_fma(a, a, f2_mul(b, b)), s0, s1);
+            f2_unpack(s, s0, s1);
             sum += (double)(s0 + s1);
         }
         return sum;
@@ -222,16 +250,49 @@ __global__ void __launch_bounds__(NR_THREADS, 5)
         r = rsqrt_fp64(sum / (double)(q.H * D) + (double)p.eps);
     }
     if (t >= rows) return;
+    // r c, r s and -r s: once a token, or once a head's unit
+    uint64_t cr[4], sr[4], nr[4];
+    auto scale_table = [&]() {
+        const uint64_t r2 = f2_splat((float)r), m2 = f2_splat(-(float)r);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) cr[k] = f2_mul(cs[k], r2), sr[k] = f2_mul(sn[k], r2), nr[k] = f2_mul(sn[k], m2);
+    };
+    if (TOKEN) scale_table();
+
+    constexpr int G = OUT == NR_NVFP4 ? 16 : 32;  // FP4: elements a scale
+    constexpr int APR = OUT == NR_NVFP4 ? 2 : 1;  // and scale atoms per 128 tokens of a head
+    const int h0 = first / LPH, dh = stride / LPH;
+    const float* const weight = q.weight;
+    // where a lane's results go, moved on by `dh` heads from unit to unit
+    __nv_bfloat16* dst = OUT == NR_BF16 ? q.out + t * q.out_stride + h0 * D : nullptr;
+    uint8_t *crow = nullptr, *srow = nullptr;
+    int64_t crow_step = 0, srow_step = 0;
+    if (OUT != NR_BF16) {
+        crow = q.codes + (h0 * rows + t) * 64;
+        crow_step = dh * rows * 64;
+        // (a scale block's first two lanes write a byte each, of chunk 0 and of chunk 1)
+        const int block = (part & 1 ? e1 : e0) / G;
+        srow = q.sf + h0 * rows * (128 / G) + sf_word_offset(t, block / 4, APR) + block % 4;
+        srow_step = dh * rows * (128 / G);
+    }
 
 #pragma unroll 1
-    for (int i = 0; i < iters; ++i) {
+    for (int i = 0; i < iters; ++i, dst += dh * D, crow += crow_step, srow += srow_step) {
         const int u = first + i * stride;
         // whole warps leave together (the shuffles below): the first lane's unit is the lowest
         if (u - lane >= units) break;
         const bool mine = u < units;
-        const int h = u / LPH;
+        const int h = h0 + i * dh;
+        if (OUT != NR_BF16 && !real) {  // padding tokens hold zero codes and scales
+            if (mine) {
+                *reinterpret_cast<uint32_t*>(crow + e0 / 2) = 0u;
+                *reinterpret_cast<uint32_t*>(crow + e1 / 2) = 0u;
+                if (part % (G / 8) < 2) *srow = 0u;
+            }
+            continue;
+        }
         uint32_t x[8];
-        if (mine && real) {
+        if (mine) {
             unit(i, x);
         } else {
 #pragma unroll
@@ -243,49 +304,58 @@ __global__ void __launch_bounds__(NR_THREADS, 5)
             for (int o = LPH / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
             r = rsqrt_fp64(sum * (1.0 / D) + (double)p.eps);
         }
-        const uint64_t r2 = f2_splat((float)r);
-        const float* const wp = q.weight && mine ? q.weight + (TOKEN ? h * D : 0) : nullptr;
-        uint64_t w[8];  // the weights of chunk 0 and chunk 1 as fp32 pairs
+        if (!TOKEN) scale_table();
+        const float* const wp = weight ? weight + (TOKEN && mine ? h * D : 0) : nullptr;
+        // Rotation pairs j = 2k and 2k + 1 are (a, b), times their weights.  In memory order their four
+        // values are a b a b (interleaved), or the two a's in chunk 0 and the two b's in chunk 1 (half).
+        uint64_t a[4], b[4];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) w[k] = f2_splat(1.0f);
+        for (int k = 0; k < 4; ++k) {
+            if (HALF) {
+                a[k] = f2_pack(bf16_lo(x[k]), bf16_hi(x[k]));
+                b[k] = f2_pack(bf16_lo(x[4 + k]), bf16_hi(x[4 + k]));
+            } else {
+                a[k] = f2_pack(bf16_lo(x[2 * k]), bf16_lo(x[2 * k + 1]));
+                b[k] = f2_pack(bf16_hi(x[2 * k]), bf16_hi(x[2 * k + 1]));
+            }
+        }
         if (wp) {
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 const float4 f = __ldg(reinterpret_cast<const float4*>(wp + (c < 2 ? e0 : e1 - 8) + 4 * c));
-                w[2 * c] = f2_pack(f.x, f.y), w[2 * c + 1] = f2_pack(f.z, f.w);
+                if (HALF) {
+                    uint64_t* const to = c < 2 ? a + 2 * c : b + 2 * c - 4;
+                    to[0] = f2_mul(to[0], f2_pack(f.x, f.y)), to[1] = f2_mul(to[1], f2_pack(f.z, f.w));
+                } else {  // (in single products: pairs of weights would have to be put together first)
+                    float x0, x1;
+                    f2_unpack(a[c], x0, x1);
+                    a[c] = f2_pack(__fmul_rn(x0, f.x), __fmul_rn(x1, f.z));
+                    f2_unpack(b[c], x0, x1);
+                    b[c] = f2_pack(__fmul_rn(x0, f.y), __fmul_rn(x1, f.w));
+                }
             }
+        }
+        auto turn = [&](int k) {
+            const uint64_t u = f2_fma(a[k], cr[k], f2_mul(b[k], nr[k]));
+            b[k] = f2_fma(a[k], sr[k], f2_mul(b[k], cr[k]));
+            a[k] = u;
+        };
+        auto keep = [&](int k) { a[k] = f2_mul(a[k], cr[k]), b[k] = f2_mul(b[k], cr[k]); };
+        // (unrotated pairs do not take c = 1, s = 0: an infinity stays alone)
+        if (p.rot == D) {
+            turn(0), turn(1), turn(2), turn(3);
+        } else {
+            if (turned0) turn(0), turn(1);
+            else keep(0), keep(1);
+            if (turned1) turn(2), turn(3);
+            else keep(2), keep(3);
         }
 
         // the unit's sixteen values as bf16, y[k] in memory order: chunk 0, then chunk 1
         uint32_t y[8], again = 0u;
 #pragma unroll
-        for (int k = 0; k < 8; k += 2) {
-            // rotation pairs j = k and k + 1 are (a, b); in memory order these four values are
-            // a b a b (interleaved), or the two a's in chunk 0 and the two b's in chunk 1
-            float a[2], b[2];
-            if (HALF) {
-                f2_unpack(f2_mul(f2_pack(bf16_lo(x[k / 2]), bf16_hi(x[k / 2])), f2_mul(w[k / 2], r2)), a[0], a[1]);
-                f2_unpack(f2_mul(f2_pack(bf16_lo(x[4 + k / 2]), bf16_hi(x[4 + k / 2])), f2_mul(w[4 + k / 2], r2)), b[0],
-                          b[1]);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-                    f2_unpack(f2_mul(f2_pack(bf16_lo(x[k + e]), bf16_hi(x[k + e])), f2_mul(w[k + e], r2)), a[e], b[e]);
-            }
-            uint32_t z[2];  // (u, v) of each pair
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const float c = cs[2 * (k + e)], sn = cs[2 * (k + e) + 1];
-                float uu = __fmaf_rn(a[e], c, -__fmul_rn(b[e], sn));
-                float vv = __fmaf_rn(a[e], sn, __fmul_rn(b[e], c));
-                if (!(k < 4 ? turned0 : turned1)) uu = a[e], vv = b[e];  // (not by c = 1, s = 0: an infinity stays alone)
-                uint32_t high;
-                z[e] = low_high(uu, vv, high);
-                again |= z[e] != high ? 1u << (k + e) : 0u;
-            }
-            y[HALF ? k / 2 : k] = HALF ? __byte_perm(z[0], z[1], 0x5410) : z[0];
-            y[HALF ? 4 + k / 2 : k + 1] = HALF ? __byte_perm(z[0], z[1], 0x7632) : z[1];
-        }
+        for (int k = 0; k < 4; ++k)
+            again |= low_high<HALF>(a[k], b[k], y[HALF ? k : 2 * k], y[HALF ? 4 + k : 2 * k + 1]) << (2 * k);
         while (again) {
             const int j = __ffs((int)again) - 1;
             again &= again - 1;
@@ -293,11 +363,11 @@ __global__ void __launch_bounds__(NR_THREADS, 5)
             const int i0 = HALF ? e0 + j : (j < 4 ? e0 : e1 - 8) + 2 * j, i1 = HALF ? e1 + j : i0 + 1;
             const uint16_t* xs = reinterpret_cast<const uint16_t*>(mine_at + i * 64 + (!HALF && j >= 4 ? 32 : 0));
             const uint32_t b0 = xs[HALF ? j : 2 * (j & 3)], b1 = HALF ? xs[32 * 8 + j] : xs[2 * (j & 3) + 1];
+            const bool turned = j < 4 ? turned0 : turned1;
             float2 csj = make_float2(1.0f, 0.0f);
-            if (j < 4 ? turned0 : turned1)
-                csj = __ldg(reinterpret_cast<const float2*>(row + (HALF ? c0 : j < 4 ? c0 : c1 - 8) + 2 * j));
+            if (turned) csj = __ldg(reinterpret_cast<const float2*>(row + (HALF ? c0 : j < 4 ? c0 : c1 - 8) + 2 * j));
             const uint32_t z = rot_exact(__uint_as_float(b0 << 16), __uint_as_float(b1 << 16), wp ? __ldg(wp + i0) : 1.0f,
-                                         wp ? __ldg(wp + i1) : 1.0f, r, csj.x, csj.y);
+                                         wp ? __ldg(wp + i1) : 1.0f, r, turned, csj.x, csj.y);
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
                 if (!HALF && k == j) y[k] = z;
@@ -310,63 +380,50 @@ __global__ void __launch_bounds__(NR_THREADS, 5)
 
         if constexpr (OUT == NR_BF16) {
             if (mine) {
-                __nv_bfloat16* dst = q.out + t * q.out_stride + h * D;
                 *reinterpret_cast<uint4*>(dst + e0) = make_uint4(y[0], y[1], y[2], y[3]);
                 *reinterpret_cast<uint4*>(dst + e1) = make_uint4(y[4], y[5], y[6], y[7]);
             }
         } else {
             // ---- FP4: blocks of G consecutive elements, as the activation quantizer
-            constexpr int G = OUT == NR_NVFP4 ? 16 : 32;
-            float v[16], top[2] = {0.0f, 0.0f};
+            // A block's values lie in the same chunk of two or four neighbouring lanes: the largest of
+            // chunk 0 in the low half of a word, of chunk 1 in the high half (a NaN beside others drops
+            // out, as in fmaxf).
+            uint32_t m0 = y[0], m1 = y[4];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                // padding tokens hold zero codes and scales
-                v[2 * k] = real ? bf16_lo(y[k]) : 0.0f, v[2 * k + 1] = real ? bf16_hi(y[k]) : 0.0f;
-                top[k / 4] = fmaxf(top[k / 4], fmaxf(fabsf(v[2 * k]), fabsf(v[2 * k + 1])));
-            }
-            // a block's values lie in the same chunk of two or four neighbouring lanes
+            for (int k = 1; k < 4; ++k) m0 = bf16_absmax2(m0, y[k]), m1 = bf16_absmax2(m1, y[4 + k]);
+            uint32_t both = bf16_absmax2(__byte_perm(m0, m1, 0x5410), __byte_perm(m0, m1, 0x7632));
 #pragma unroll
-            for (int o = 1; o < G / 8; o <<= 1) {
-                top[0] = fmaxf(top[0], __shfl_xor_sync(0xffffffffu, top[0], o));
-                top[1] = fmaxf(top[1], __shfl_xor_sync(0xffffffffu, top[1], o));
+            for (int o = 1; o < G / 8; o <<= 1)
+                both = bf16_absmax2(both, __shfl_xor_sync(0xffffffffu, both, o));
+            both &= 0x7FFF7FFFu;
+            const float top[2] = {fmaxf(bf16_lo(both), 0.0f), fmaxf(bf16_hi(both), 0.0f)};
+            uint32_t cw[2], sfb[2];
+            if (OUT == NR_NVFP4) {
+                // top / (6 g) rounded to e4m3: within 2^-23 from the reciprocal, so where both ends of a
+                // wider band give one byte that is it, else (and for extreme g) the division
+                const float f0 = top[0] * per_six_g, f1 = top[1] * per_six_g;
+                const uint32_t low = cvt_e4m3x2(f0 * (1.0f - 0x1p-21f), f1 * (1.0f - 0x1p-21f));
+                uint32_t two = cvt_e4m3x2(f0 * (1.0f + 0x1p-21f), f1 * (1.0f + 0x1p-21f));
+                if (low != two || per_six_g == 0.0f)
+                    two = cvt_e4m3x2(__fdiv_rn(top[0], six_g), __fdiv_rn(top[1], six_g));
+                sfb[0] = two & 0xFFu, sfb[1] = two >> 8;
+            } else {
+                sfb[0] = mx_scale_byte<2>(top[0]), sfb[1] = mx_scale_byte<2>(top[1]);
             }
-            uint32_t cw[2], words[2] = {0u, 0u};
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
+                const float rr = OUT == NR_NVFP4 ? nv_rcp[sfb[c] & 0x7Fu] : mx_inv_scale(sfb[c]);
                 float z[8];
-                uint32_t sfb;
-                if (OUT == NR_NVFP4) {
-                    sfb = cvt_e4m3x2(__fdiv_rn(top[c], six_g), 0.0f) & 0xFFu;
-                    const float rr = nv_rcp[sfb & 0x7Fu];
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) z[k] = rr == 0.0f ? 0.0f : __fmul_rn(v[8 * c + k], rr);
-                } else {
-                    sfb = mx_scale_byte<2>(top[c]);
-                    const float inv = mx_inv_scale(sfb);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) z[k] = __fmul_rn(v[8 * c + k], inv);
-                }
-                cw[c] = cvt_e2m1x8(z);
-                const int block = (c ? e1 : e0) / G;
-                if (G == 16) {
-                    words[0] |= block < 4 ? sfb << (8 * block) : 0u;
-                    words[1] |= block >= 4 ? sfb << (8 * (block - 4)) : 0u;
-                } else {
-                    words[0] |= sfb << (8 * block);
-                }
-            }
-#pragma unroll
-            for (int o = 1; o < LPH; o <<= 1) {
-                words[0] |= __shfl_xor_sync(0xffffffffu, words[0], o);
-                if (G == 16) words[1] |= __shfl_xor_sync(0xffffffffu, words[1], o);
+                for (int k = 0; k < 4; ++k)
+                    f2_unpack(f2_mul(f2_pack(bf16_lo(y[4 * c + k]), bf16_hi(y[4 * c + k])), f2_splat(rr)), z[2 * k],
+                              z[2 * k + 1]);
+                cw[c] = rr == 0.0f ? 0u : cvt_e2m1x8(z);  // (NVFP4: scale zero)
             }
             if (mine) {
-                uint8_t* crow = q.codes + ((int64_t)h * rows + t) * 64;
                 *reinterpret_cast<uint32_t*>(crow + e0 / 2) = cw[0];
                 *reinterpret_cast<uint32_t*>(crow + e1 / 2) = cw[1];
-                constexpr int APR = G == 16 ? 2 : 1;  // scale atoms per 128 tokens of a head
-                uint8_t* srow = q.sf + (int64_t)h * rows * (128 / G);
-                if (part < APR) *reinterpret_cast<uint32_t*>(srow + sf_word_offset(t, part, APR)) = words[part];
+                if (part % (G / 8) < 2) *srow = (uint8_t)(part & 1 ? sfb[1] : sfb[0]);
             }
         }
     }
