@@ -77,6 +77,7 @@ constexpr int AB_THREADS = 384;
 constexpr uint32_t AB_REG_LAUNCH = 168, AB_REG_LO = 72, AB_REG_HI = 216;
 static_assert(AB_REG_LO + 2 * AB_REG_HI == 3 * AB_REG_LAUNCH, "register split must match the launch");
 constexpr int AB_KEYS = 128;  // keys of a tile
+constexpr int AB_ITEMS = 4;   // items in flight between the planner and the slowest warp
 constexpr float AB_LAZY = 8.0f;  // log2 of how far P may exceed 1
 
 template <int D>
@@ -172,13 +173,14 @@ FP4_DEV uint64_t tanh_near(uint64_t s, const float (&t)[6]) {
 
 // An item as the planner gives it to the other warps
 struct AttnBfItem {
+    int t0, hk, z, subs; // first token, key head, part; row tiles
+    int t0_next;         // first token of the CTA's next item (T_q: none)
     int jb, n;           // its key tiles
     int see_lo, see_hi;  // the keys that all its rows see
     int bad;             // set by the guard: a guarded V tile held an infinity or a NaN
     // tiles that some row does not see whole (keys beyond T_kv are zeros already)
     FP4_DEV bool guarded(int j, int T_kv) const { return j * 128 < see_lo || min(j * 128 + 128, T_kv) > see_hi; }
 };
-constexpr int AB_ITEMS = 4;  // items in flight between the planner and the slowest warp
 
 template <int D, bool CAP, bool BIAS>
 __global__ void __launch_bounds__(AB_THREADS, 1)
@@ -208,7 +210,7 @@ __global__ void __launch_bounds__(AB_THREADS, 1)
                                        // side laps the other: the ring holds 4 at most
     uint64_t* item_full = q_full + 18;             // [AB_ITEMS] item planned
     uint64_t* item_empty = item_full + AB_ITEMS;   // [AB_ITEMS] all warps are done with it
-    uint64_t* mma_done = item_empty + AB_ITEMS;    
+    uint64_t* mma_done = item_empty + AB_ITEMS;
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(mma_done + 1);
     volatile int* abort = reinterpret_cast<volatile int*>(tmem_holder + 1);
     volatile AttnBfItem* info = reinterpret_cast<volatile AttnBfItem*>(sm + C::OFF_MISC + 512);  // [AB_ITEMS]
@@ -295,6 +297,7 @@ __global__ void __launch_bounds__(AB_THREADS, 1)
                     ks[i] = in ? (p.key_start ? p.key_start[t] : 0) : INT_MAX;
                     ke[i] = in ? (p.key_end ? p.key_end[t] : p.T_kv) : INT_MIN;
                 }
+                return t0;
             };
             fetch(item_of(0));
             for (int k = 0; ok; ++k) {
@@ -314,17 +317,19 @@ __global__ void __launch_bounds__(AB_THREADS, 1)
                 hi = __reduce_max_sync(0xffffffffu, hi);
                 all_lo = __reduce_max_sync(0xffffffffu, all_lo);
                 all_hi = __reduce_min_sync(0xffffffffu, all_hi);
-                fetch(item_of(k + 1));
                 int jb = 0, n = 0;
                 if (lo < hi) {
                     const int first = lo / 128, all = (hi + 127) / 128 - first;
                     jb = first + (int)((int64_t)all * at.z / p.splits);
                     n = first + (int)((int64_t)all * (at.z + 1) / p.splits) - jb;
                 }
+                const int e = k % AB_ITEMS;
+                ok = mbar_wait_warp(&item_empty[e], (uint32_t)((k / AB_ITEMS) & 1) ^ 1u, p.timeout_ns, abort);
+                const int t0_next = fetch(item_of(k + 1));
                 if (lane == 0) {
-                    const int e = k % AB_ITEMS;
-                    ok = mbar_wait(&item_empty[e], (uint32_t)((k / AB_ITEMS) & 1) ^ 1u, p.timeout_ns, abort);
                     if (ok) {
+                        info[e].t0 = at.t0, info[e].hk = at.hk, info[e].z = at.z, info[e].subs = subs_of(at);
+                        info[e].t0_next = t0_next;
                         info[e].jb = jb, info[e].n = n, info[e].see_lo = all_lo, info[e].see_hi = all_hi, info[e].bad = 0;
                         mbar_arrive(&item_full[e]);
                     }
@@ -400,11 +405,11 @@ __global__ void __launch_bounds__(AB_THREADS, 1)
                 return true;
             };
             for (int k = 0; ok; ++k) {
-                const int item = item_of(k), e = k % AB_ITEMS;
-                if (item >= p.items) break;
+                const int e = k % AB_ITEMS;
+                if (item_of(k) >= p.items) break;
                 ok = wait(&item_full[e], (uint32_t)((k / AB_ITEMS) & 1));
                 if (!ok) break;
-                const int n = __reduce_max_sync(0xffffffffu, info[e].n), nsub = subs_of(place(item));
+                const int n = __reduce_max_sync(0xffffffffu, info[e].n), nsub = __reduce_max_sync(0xffffffffu, info[e].subs);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&item_empty[e]);
                 __syncwarp();
@@ -508,32 +513,31 @@ __global__ void __launch_bounds__(AB_THREADS, 1)
         uint32_t ns = 0, no = 0;  // S tiles and O results so far
         bool ok = true;
         // a row's token in an item, or -1, and its range
-        auto token_of = [&](const Place& at) {
-            const int t = at.t0 + (p.alt ? 0 : w * p.tokens) + row_tok;
+        auto token_of = [&](int t0) {
+            const int t = t0 + (p.alt ? 0 : w * p.tokens) + row_tok;
             return row_tok < p.tokens && t < p.T_q ? t : -1;
         };
         int ks_next = 0, ke_next = p.T_kv;
-        auto fetch = [&](int item) {
-            if (!guarding || item >= p.items) return;
-            const int t = token_of(place(item));
+        auto fetch = [&](int t0) {
+            if (!guarding) return;
+            const int t = token_of(t0);
             ks_next = t >= 0 && p.key_start ? p.key_start[t] : 0;
             ke_next = t >= 0 && p.key_end ? p.key_end[t] : p.T_kv;
         };
-        fetch(item_of(0));
+        if (item_of(0) < p.items) fetch(place(item_of(0)).t0);
         for (int k = 0; ok; ++k) {
-            const int item = item_of(k), e = k % AB_ITEMS;
-            if (item >= p.items) break;
-            const Place at = place(item);
-            const int tok = token_of(at), head = at.hk * p.g + row_head;
+            const int e = k % AB_ITEMS;
+            if (item_of(k) >= p.items) break;
+            ok = mbar_wait_warp(&item_full[e], (uint32_t)((k / AB_ITEMS) & 1), p.timeout_ns, abort);
+            if (!ok) break;
+            const int tok = token_of(info[e].t0), head = info[e].hk * p.g + row_head;
             int ks = max(ks_next, 0), ke = min(ke_next, p.T_kv);
             const bool row_some = tok >= 0 && ks < ke;
             if (!row_some) ks = 0, ke = p.T_kv;  // masks nothing; its output is not taken from O
+            fetch(info[e].t0_next);
             // the keys that all rows of the warp see
             const int all_lo = __reduce_max_sync(0xffffffffu, ks), all_hi = __reduce_min_sync(0xffffffffu, ke);
-            fetch(item_of(k + 1));
-            ok = mbar_wait_warp(&item_full[e], (uint32_t)((k / AB_ITEMS) & 1), p.timeout_ns, abort);
-            if (!ok) break;
-            const int jb = info[e].jb, n = w < subs_of(at) ? tiles_of(info[e].n, w) : 0;
+            const int jb = info[e].jb, n = w < info[e].subs ? tiles_of(info[e].n, w) : 0;
             float m = -INFINITY, l = 0.0f;  // the maximum that P and O refer to (log2 units), the sum
             const float slope = BIAS && tok >= 0 ? -1.44269504f * p.slopes[head] : 0.0f;
             for (int i = 0; ok && i < n; ++i, ++ns) {
@@ -675,7 +679,7 @@ __global__ void __launch_bounds__(AB_THREADS, 1)
             const bool some = row_some && n > 0, bad = info[e].bad != 0;
             const float inv = some && p.parts == 1 ? 1.0f / l : 1.0f;
             const size_t row = (size_t)tok * p.H + head;
-            const size_t part = (size_t)(p.alt ? 2 * at.z + w : at.z) * p.T_q * p.H + row;
+            const size_t part = (size_t)(p.alt ? 2 * info[e].z + w : info[e].z) * p.T_q * p.H + row;
 #pragma unroll
             for (int b = 0; b < D / 32; ++b) {
                 uint32_t o[32];
@@ -701,7 +705,7 @@ __global__ void __launch_bounds__(AB_THREADS, 1)
                         if (!wk.guarded(j, p.T_kv)) continue;
 #pragma unroll 1
                         for (int key = max(ks, j * 128); key < min(ke, j * 128 + 128); ++key) {
-                            const __nv_bfloat16* src = p.v + key * p.v_stride + at.hk * D + 32 * b;
+                            const __nv_bfloat16* src = p.v + key * p.v_stride + info[e].hk * D + 32 * b;
 #pragma unroll
                             for (int y = 0; y < 32; ++y) {
                                 const float x = __bfloat162float(src[y]);
