@@ -723,6 +723,19 @@ def _launch(dev: int, call, *args):
             call(*args)
 
 
+def _new(dev: int, stream, make):
+    """make()'s tensor, allocated on `stream` where one is given: its memory may have been another
+    tensor's of the current stream, and a workspace goes back to the allocator when the helper returns."""
+    if stream is None:
+        return make()
+    import torch
+
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=dev) if int(stream) else torch.cuda.default_stream(dev)
+    with torch.cuda.stream(stream):
+        return make()
+
+
 def rope_table(positions, axis_dims, theta: float = 10000.0, factor: float = 1.0, window: int = 0,
                amplitude: float = 1.0, table=None, stream=None):
     """Rotary table of int32 positions [T, axes] (CUDA): fp32 [T, sum(axis_dims)] (cos, sin) pairs."""
@@ -733,7 +746,7 @@ def rope_table(positions, axis_dims, theta: float = 10000.0, factor: float = 1.0
     dev, T = positions.get_device(), positions.shape[0]
     pos = _expect(positions, "positions", torch.int32, dev)
     if table is None:
-        table = torch.empty((T, sum(axis_dims)), dtype=torch.float32, device=positions.device)
+        table = _new(dev, stream, lambda: torch.empty((T, sum(axis_dims)), dtype=torch.float32, device=positions.device))
     _launch(dev, fp4_rope_table, pos, T, len(axis_dims), axis_dims, theta, factor, window, amplitude,
             _expect(table, "table", torch.float32, dev, (T, sum(axis_dims))), stream)
     return table
@@ -768,14 +781,14 @@ def qk_norm_rope(q, k=None, norm="head", q_weight=None, k_weight=None, eps: floa
     args = _norm_rope_args(q, k, norm, q_weight, k_weight, eps, table, layout)
     dev = q.get_device()
     if q_out is None:
-        q_out = q.new_empty(q.shape)
+        q_out = _new(dev, stream, lambda: q.new_empty(q.shape))
     if k is None:
         if k_out is not None:
             raise ValueError("k_out without k")
         outs = (*_expect_rows(q_out, "q_out", dev, q.shape), None, 0)
     else:
         if k_out is None:
-            k_out = k.new_empty(k.shape)
+            k_out = _new(dev, stream, lambda: k.new_empty(k.shape))
         outs = (*_expect_rows(q_out, "q_out", dev, q.shape), *_expect_rows(k_out, "k_out", dev, k.shape))
     _launch(dev, fp4_qk_norm_rope, *args, *outs, stream)
     return q_out if k is None else (q_out, k_out)
@@ -794,8 +807,9 @@ def qk_norm_rope_quantize_heads(q, k=None, fmt="mxfp4", norm="head", q_weight=No
     outs, ptrs = [], []
     for x in (q,) if k is None else (q, k):
         H = x.shape[1]
-        codes = torch.empty((H, Tpad, D // 2), dtype=torch.uint8, device=q.device)
-        sf = torch.empty((H, Tpad * (D // (32 if f == MXFP4 else 16))), dtype=torch.uint8, device=q.device)
+        codes = _new(dev, stream, lambda: torch.empty((H, Tpad, D // 2), dtype=torch.uint8, device=q.device))
+        sf = _new(dev, stream,
+                  lambda: torch.empty((H, Tpad * (D // (32 if f == MXFP4 else 16))), dtype=torch.uint8, device=q.device))
         outs.append((codes, sf))
         ptrs += [codes.data_ptr(), sf.data_ptr()]
     if k is None:
@@ -818,7 +832,7 @@ def dequantize_heads(heads, T: int, fmt="mxfp4", g=None, x=None, stream=None):
     cp = _expect(codes, "codes", torch.uint8, dev)
     sp = _expect(sf, "scales", torch.uint8, dev, (H, Tpad * (2 * half_d // (32 if f == MXFP4 else 16))))
     if x is None:
-        x = torch.empty((T, H, 2 * half_d), dtype=torch.bfloat16, device=codes.device)
+        x = _new(dev, stream, lambda: torch.empty((T, H, 2 * half_d), dtype=torch.bfloat16, device=codes.device))
     _launch(dev, fp4_dequantize_heads, f, cp, sp, T, H, 2 * half_d, _expect(g, "g", torch.float32, dev),
             *_expect_rows(x, "x", dev, (T, H, 2 * half_d)), stream)
     return x
@@ -841,12 +855,17 @@ def linear_residual(x, pw: PackedWeight, residual=None, bias=None, act="none", g
     xp = _expect(x, "x", torch.bfloat16, dev)
     rp = _expect(residual, "residual", torch.bfloat16, dev, (M, N))
     bp = _expect(bias, "bias", torch.float16, dev, (N,))
+    wp = _expect(pw.codes, "weight codes", torch.uint8, dev, (N, K // 2))
+    wsp, wgp = _expect(pw.sf, "weight scales", torch.uint8, dev), _expect(pw.w_global, "w_global", torch.float32, dev)
+    if pw.sf.numel() != fp4_sf_bytes(pw.fmt, N, K):
+        raise ValueError(f"weight scales: expected {fp4_sf_bytes(pw.fmt, N, K)} bytes, got {pw.sf.numel()}")
     gp = None if gate is None else _expect(gate, "gate", torch.float32, dev, (-(-M // gate_rows), N))
     if y is None:
-        y = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+        y = _new(dev, stream, lambda: torch.empty((M, N), dtype=torch.bfloat16, device=x.device))
     if workspace is None:
-        workspace = torch.empty(fp4_linear_workspace_bytes(pw.fmt, M, K, N), dtype=torch.uint8, device=x.device)
-    _launch(dev, fp4_linear_residual, pw.fmt, xp, M, K, N, pw.codes, pw.sf, pw.w_global,
+        size = fp4_linear_workspace_bytes(pw.fmt, M, K, N)
+        workspace = _new(dev, stream, lambda: torch.empty(size, dtype=torch.uint8, device=x.device))
+    _launch(dev, fp4_linear_residual, pw.fmt, xp, M, K, N, wp, wsp, wgp,
             _expect(a_global, "a_global", torch.float32, dev), bp, act, gp, gate_rows, rp,
             _expect(y, "y", torch.bfloat16, dev, (M, N)), _expect(workspace, "workspace", torch.uint8, dev),
             workspace.numel(), stream)
@@ -862,7 +881,7 @@ def attn_ranges(q_offsets, k_offsets, T_q: int, T_kv: int, causal=False, prefix=
     qp = _expect(q_offsets, "q_offsets", torch.int32, dev, (docs + 1,))
     kp = _expect(k_offsets, "k_offsets", torch.int32, dev, (docs + 1,))
     pp = _expect(prefix, "prefix", torch.int32, dev, (docs,))
-    start, end = q_offsets.new_empty(T_q), q_offsets.new_empty(T_q)
+    start, end = (_new(dev, stream, lambda: q_offsets.new_empty(T_q)) for _ in range(2))
     _launch(dev, fp4_attn_ranges, qp, kp, docs, T_q, T_kv, causal, pp, start.data_ptr(), end.data_ptr(), stream)
     return start, end
 
@@ -884,12 +903,14 @@ def attn_bf16(q, k, v, scale: float, softcap: float = 0.0, slopes=None, q_pos: i
         raise ValueError(f"k: expected [T_kv, H_kv, {D}], got {tuple(k.shape)}")
     vp, v_stride = _expect_rows(v, "v", dev, k.shape)
     if o is None:
-        o = q.new_empty(q.shape)
+        o = _new(dev, stream, lambda: q.new_empty(q.shape))
     op, o_stride = _expect_rows(o, "o", dev, q.shape)
-    lse = torch.empty((T_q, H), dtype=torch.float32, device=q.device) if return_lse else None
+    lse = None
+    if return_lse:
+        lse = _new(dev, stream, lambda: torch.empty((T_q, H), dtype=torch.float32, device=q.device))
     ws = fp4_attn_bf16_workspace_bytes(T_q, T_kv, H, H_kv, D)
     if workspace is None and ws:
-        workspace = torch.empty(ws, dtype=torch.uint8, device=q.device)
+        workspace = _new(dev, stream, lambda: torch.empty(ws, dtype=torch.uint8, device=q.device))
     wp = _expect(workspace, "workspace", torch.uint8, dev)
     _launch(dev, fp4_attn_bf16, qp, q_stride, T_q, kp, k_stride, vp, v_stride, T_kv, H, H_kv, D, scale, softcap,
             _expect(slopes, "slopes", torch.float32, dev, (H,)), q_pos,
