@@ -7,8 +7,9 @@ arithmetic runs in the library's CUDA kernels.  There is no fallback: if the
 library is missing or the device is not sm_100, the calls raise.
 
 The helpers at the end (pack_weight, calibrate_act_global, quantize_act, linear, w4a8_linear,
-w4a4_linear, gelu_quantize_act, linear_gelu_quant, linear_host)
-allocate outputs and workspaces with torch and call the same entry points.
+w4a4_linear, gelu_quantize_act, linear_gelu_quant, linear_host, and around the attention
+rope_table, qk_norm_rope, qk_norm_rope_quantize_heads, dequantize_heads, linear_residual,
+attn_ranges, attn_bf16) allocate outputs and workspaces with torch and call the same entry points.
 """
 from __future__ import annotations
 

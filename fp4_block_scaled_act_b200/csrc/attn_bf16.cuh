@@ -24,6 +24,15 @@
 // O is rescaled in TMEM, by the softmax warps, which know from S's arrival that the last P V is done.
 // What bounds it: per 128 x 128 scores 512 cycles of MMA for S and for P V each (head_dim 128), and
 // 16384 exponentials at 16 a cycle, 1024 cycles, in turn for a row tile, in parallel for the two.
+// Measured, head_dim 128: 8192 rows x 8192 keys x 16 heads 553 us (994 TFLOP/s, 0.60 of the library
+// GEMM's rate), causal 283 (972), capped 807, with a bias 708; head_dim 64 507.  The tensor pipe is
+// busy 0.54 of the cycles, the exponentials' pipe as much: what is left is each row tile's chain from
+// S over its maximum and exponentials to P V, which the other tile covers only in part.  Tried and no
+// faster: 64-key tiles, a reference maximum guessed ahead, exponentials by polynomial for a share of
+// the keys, P handed over whole, a second MMA warp, O staged through shared memory.
+// Few keys: 32760 rows x 40 heads over 512 keys 447 us, over 256 302 (104 us of bytes): an item of
+// one key tile takes a softmax warp some 8000 cycles in turn, of which 3600 go to reading and
+// storing O.  One token x 40 heads (8 key heads) over 100001 keys: 94 us (62 of bytes).
 //
 // Masks cost only where they cut: tiles outside every row's range are not visited, a warp whose
 // 32 rows see a whole tile does not test keys.  Within a tile that some row does not see whole,

@@ -7,11 +7,20 @@
 //   (u, v) -> (u c_j - v s_j, u s_j + v c_j)     for the pairs j of the first R elements:
 //       interleaved: elements 2j, 2j + 1;  half: elements j, j + R / 2.
 //
-// The output is the nearest bf16 of that value (rot_pair), so the FP4 form, which quantizes
+// The output is the nearest bf16 of that value (low_high, rot_exact), so the FP4 form, which quantizes
 // that bf16, gives the codes and scales that the head quantizer gives for the bf16 form's output,
 // and neither depends on how the fp32 arithmetic in between is ordered.  The sum of squares is
-// taken in fp32 for two elements at a time (their squares are exact there, the sum of two is
-// rounded once) and in fp64 above that, so the root is within a relative 2^-24 in every case.
+// taken in fp32 for eight elements at a time (their squares are exact there) and in fp64 above
+// that: four roundings of positive terms, so the root is within a relative 2^-23 in every case.
+//
+// What bounds it: instructions.  75600 tokens of 40 + 40 heads of 128 move 3.1 GB in the bf16 form, 477 us
+// at the copy rate, and take 614 (5.0 TB/s); with NVFP4 out 2.0 GB, 302 us, and 760, at 385 warp
+// instructions for 512 elements and 0.65 of the issue slots.  Of those 385 the fp64 path of the
+// pairs that fp32 leaves open takes some 80, quantization 90, the sum of squares 26, the rotation 16.
+// What was taken out: the root goes into the table's entries, once a token instead of once a weight;
+// pairs of pairs are rotated in packed fp32; scale bytes are stored one by one instead of gathered by
+// shuffles; the interleaved layout multiplies its weights singly, since packed products would
+// first need them regrouped.  Persistent blocks with the weights in shared memory were slower (975).
 //
 // Work unit: 16 elements of one head, as two 16-byte chunks half a head apart (half layout: the
 // two that rotate together).  D / 16 consecutive lanes hold a head, so each load and store of a
@@ -37,7 +46,8 @@ struct RopeFreqs {
 // within 2^-65, |p| at most 2^31, and the host's frequency within a few 2^-53 of itself: 2^-24 of
 // a turn at the far end for the fastest pair); its upper 32 bits, a signed number of half turns,
 // are rounded to fp32 (2^-25) and go to sincospif.  Integer arithmetic instead of fp64 products:
-// 75600 x 64 pairs took 74 us with those.  A thread keeps its pair and walks over the tokens.
+// 75600 x 64 pairs took 74 us with those and take 14 (38.7 MB written, 6 us at the copy rate; the
+// rest is sincospif).  A thread keeps its pair and walks over the tokens.
 __global__ void __launch_bounds__(256) rope_table_kernel(const int32_t* __restrict__ pos, int64_t T, int axes,
                                                          int pairs, float amplitude,
                                                          const __grid_constant__ RopeFreqs f,
@@ -366,8 +376,9 @@ __global__ void __launch_bounds__(NR_THREADS, 5)
             const bool turned = j < 4 ? turned0 : turned1;
             float2 csj = make_float2(1.0f, 0.0f);
             if (turned) csj = __ldg(reinterpret_cast<const float2*>(row + (HALF ? c0 : j < 4 ? c0 : c1 - 8) + 2 * j));
-            const uint32_t z = rot_exact(__uint_as_float(b0 << 16), __uint_as_float(b1 << 16), wp ? __ldg(wp + i0) : 1.0f,
-                                         wp ? __ldg(wp + i1) : 1.0f, r, turned, csj.x, csj.y);
+            const float w0 = wp ? __ldg(wp + i0) : 1.0f, w1 = wp ? __ldg(wp + i1) : 1.0f;
+            const uint32_t z = rot_exact(__uint_as_float(b0 << 16), __uint_as_float(b1 << 16), w0, w1, r, turned, csj.x,
+                                         csj.y);
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
                 if (!HALF && k == j) y[k] = z;
@@ -434,7 +445,8 @@ __global__ void __launch_bounds__(NR_THREADS, 5)
 // times its scale (NVFP4: the scale times the global, rounded to fp32), rounded once more.  A block
 // takes 64 tokens of one head, a thread 8 values (4 code bytes in, 16 bytes out) of four tokens.
 // The code's value in bf16 comes out of two byte tables by prmt: its high byte (sign apart) is one
-// of 00 3f 3f 3f 40 40 40 40, its low byte one of 00 00 80 c0 00 40 80 c0.
+// of 00 3f 3f 3f 40 40 40 40, its low byte one of 00 00 80 c0 00 40 80 c0.  Bound by the writes: 75600
+// tokens x 40 heads take 199 us for 1.0 GB (5.0 TB/s, 151 us at the copy rate).
 template <bool NV>
 __global__ void __launch_bounds__(256) dequant_heads_kernel(const uint8_t* __restrict__ codes,
                                                             const uint8_t* __restrict__ sf, int64_t T,
