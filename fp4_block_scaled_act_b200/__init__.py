@@ -713,6 +713,16 @@ def _expect_rows(t, what: str, dev: int, shape=None):
     return t.data_ptr(), row if T > 1 else H * D
 
 
+def _rows_like(out, what: str, x, dev: int, stream):
+    """(out, its address and row stride): `out` checked, or a new tensor like x [T, H, D] (rows next to one another)."""
+    if out is not None:
+        return out, *_expect_rows(out, what, dev, x.shape)
+    import torch
+
+    out = _new(dev, stream, lambda: torch.empty_like(x, memory_format=torch.contiguous_format))
+    return out, out.data_ptr(), x.shape[1] * x.shape[2]
+
+
 def _launch(dev: int, call, *args):
     """The call with CUDA device `dev` current (its stream is that device's current one)."""
     import torch
@@ -781,16 +791,14 @@ def qk_norm_rope(q, k=None, norm="head", q_weight=None, k_weight=None, eps: floa
     rope_table, or None.  Returns (q_out, k_out), or q_out alone; q_out = q rotates in place."""
     args = _norm_rope_args(q, k, norm, q_weight, k_weight, eps, table, layout)
     dev = q.get_device()
-    if q_out is None:
-        q_out = _new(dev, stream, lambda: q.new_empty(q.shape))
-    if k is None:
-        if k_out is not None:
-            raise ValueError("k_out without k")
-        outs = (*_expect_rows(q_out, "q_out", dev, q.shape), None, 0)
+    q_out, *outs = _rows_like(q_out, "q_out", q, dev, stream)
+    if k is not None:
+        k_out, *k_outs = _rows_like(k_out, "k_out", k, dev, stream)
+        outs += k_outs
+    elif k_out is not None:
+        raise ValueError("k_out without k")
     else:
-        if k_out is None:
-            k_out = _new(dev, stream, lambda: k.new_empty(k.shape))
-        outs = (*_expect_rows(q_out, "q_out", dev, q.shape), *_expect_rows(k_out, "k_out", dev, k.shape))
+        outs += [None, 0]
     _launch(dev, fp4_qk_norm_rope, *args, *outs, stream)
     return q_out if k is None else (q_out, k_out)
 
@@ -808,6 +816,11 @@ def qk_norm_rope_quantize_heads(q, k=None, fmt="mxfp4", norm="head", q_weight=No
     outs, ptrs = [], []
     for x in (q,) if k is None else (q, k):
         H = x.shape[1]
+        if outs and H == q.shape[1]:  # (a tensor like another one is the quickest to have)
+            codes, sf = (_new(dev, stream, lambda t=t: torch.empty_like(t)) for t in outs[0])
+            outs.append((codes, sf))
+            ptrs += [codes.data_ptr(), sf.data_ptr()]
+            continue
         codes = _new(dev, stream, lambda: torch.empty((H, Tpad, D // 2), dtype=torch.uint8, device=q.device))
         sf = _new(dev, stream,
                   lambda: torch.empty((H, Tpad * (D // (32 if f == MXFP4 else 16))), dtype=torch.uint8, device=q.device))
@@ -903,9 +916,7 @@ def attn_bf16(q, k, v, scale: float, softcap: float = 0.0, slopes=None, q_pos: i
     if k.shape[2] != D:
         raise ValueError(f"k: expected [T_kv, H_kv, {D}], got {tuple(k.shape)}")
     vp, v_stride = _expect_rows(v, "v", dev, k.shape)
-    if o is None:
-        o = _new(dev, stream, lambda: q.new_empty(q.shape))
-    op, o_stride = _expect_rows(o, "o", dev, q.shape)
+    o, op, o_stride = _rows_like(o, "o", q, dev, stream)
     lse = None
     if return_lse:
         lse = _new(dev, stream, lambda: torch.empty((T_q, H), dtype=torch.float32, device=q.device))
