@@ -30,9 +30,9 @@
 // S over its maximum and exponentials to P V, which the other tile covers only in part.  Tried and no
 // faster: 64-key tiles, a reference maximum guessed ahead, exponentials by polynomial for a share of
 // the keys, P handed over whole, a second MMA warp, O staged through shared memory.
-// Few keys: 32760 rows x 40 heads over 512 keys 447 us, over 256 302 (104 us of bytes): an item of
-// one key tile takes a softmax warp some 8000 cycles in turn, of which 3600 go to reading and
-// storing O.  One token x 40 heads (8 key heads) over 100001 keys: 94 us (62 of bytes).
+// Few keys: 32760 rows x 40 heads over 512 keys 423 us, over 256 281 (104 us of bytes): an item of
+// one key tile takes a softmax warp some 7000 cycles in turn, most of it the wait for S, its
+// exponentials, the wait for P V, and reading and storing O.  One token x 40 heads (8 key heads) over 100001 keys: 94 us (62 of bytes).
 //
 // Masks cost only where they cut: tiles outside every row's range are not visited, a warp whose
 // 32 rows see a whole tile does not test keys.  Within a tile that some row does not see whole,
@@ -689,7 +689,9 @@ __global__ void __launch_bounds__(AB_THREADS, 1)
             const float inv = some && p.parts == 1 ? 1.0f / l : 1.0f;
             const size_t row = (size_t)tok * p.H + head;
             const size_t part = (size_t)(p.alt ? 2 * info[e].z + w : info[e].z) * p.T_q * p.H + row;
-#pragma unroll
+            // (a loop, whose code is a quarter: 32760 rows over 512 keys took 451 us unrolled and 423 so; but capped
+            // and biased scores, 812 and 706 us at 8192 x 8192, took 842 and 727 with it)
+#pragma unroll (CAP || BIAS ? D / 32 : 1)
             for (int b = 0; b < D / 32; ++b) {
                 uint32_t o[32];
                 if (n > 0) {
