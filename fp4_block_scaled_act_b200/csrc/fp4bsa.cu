@@ -1248,13 +1248,14 @@ fp4_status_t fp4_rope_table(const int32_t* positions, int64_t T, int axes, const
     RopeFreqs f{};
     int64_t pairs = 0;
     const double two_pi = 6.283185307179586476925287;
+    const double log_theta = std::log(theta);
     for (int a = 0; a < axes; ++a) {
         const int64_t d = axis_dims[a];
         if (d < 0 || (d & 1) || pairs + d / 2 > ROPE_MAX_PAIRS) return FP4_ERR_UNSUPPORTED_SHAPE;
         // by parts: pair j turns window / wavelength_j times within the trained window; 32 turns and
         // more keep their frequency, one turn and fewer are slowed by the factor, a ramp lies between
         const auto pair_of = [&](double turns) {
-            return (double)d * std::log((double)window / (two_pi * turns)) / (2.0 * std::log(theta));
+            return (double)d * std::log((double)window / (two_pi * turns)) / (2.0 * log_theta);
         };
         double lo = 0.0, hi = 0.0;
         if (window > 0) {
@@ -1262,7 +1263,7 @@ fp4_status_t fp4_rope_table(const int32_t* positions, int64_t T, int axes, const
             hi = std::min(std::ceil(pair_of(1.0)), (double)(d - 1));
         }
         for (int64_t j = 0; j < d / 2; ++j) {
-            double w = std::pow(theta, -2.0 * (double)j / (double)d);
+            double w = std::exp(log_theta * (-2.0 * (double)j / (double)d));  // (pow took twice as long)
             if (factor != 1.0) {
                 const double ramp =
                     window > 0 ? std::min(std::max(((double)j - lo) / std::max(hi - lo, 1e-3), 0.0), 1.0) : 1.0;

@@ -57,11 +57,18 @@ __global__ void __launch_bounds__(256) rope_table_kernel(const int32_t* __restri
     if (row >= per) return;
     const uint64_t turns = f.turns[j];
     const int axis = f.axis[j];
-    for (int64_t t = (int64_t)blockIdx.x * per + row; t < T; t += (int64_t)gridDim.x * per) {
-        const uint64_t x = (uint64_t)(int64_t)pos[t * axes + axis] * turns;
+    const int64_t t0 = (int64_t)blockIdx.x * per + row, step = (int64_t)gridDim.x * per;
+    const int32_t* src = pos + t0 * axes + axis;
+    float2* dst = table + t0 * pairs + j;
+    int left = t0 < T ? (int)((T - 1 - t0) / step) + 1 : 0;  // this thread's tokens
+    int32_t next = left ? *src : 0;
+    for (; left > 0; --left, dst += step * pairs) {
+        const uint64_t x = (uint64_t)(int64_t)next * turns;
+        src += step * axes;
+        if (left > 1) next = *src;  // (while this one is worked on)
         float s, c;
         sincospif((float)(int32_t)(x >> 32) * 0x1p-31f, &s, &c);
-        __stcs(table + t * pairs + j, make_float2(__fmul_rn(amplitude, c), __fmul_rn(amplitude, s)));
+        __stcs(dst, make_float2(__fmul_rn(amplitude, c), __fmul_rn(amplitude, s)));
     }
 }
 
