@@ -43,8 +43,8 @@ struct RopeFreqs {
 
 // table[t][j] = amplitude (cos, sin)(2 pi frac(p turns_j)).  The fraction of the turn count is
 // the low 64 bits of the integer product, within 2^-34 of a turn for every position (turns_j is
-// within 2^-65, |p| at most 2^31, and the host's frequency within a few 2^-53 of itself: 2^-24 of
-// a turn at the far end for the fastest pair); its upper 32 bits, a signed number of half turns,
+// within 2^-65, |p| at most 2^31, and the host's frequency e^-x within (3 x + 1) 2^-53 of itself:
+// 2^-23 of a turn at the far end, where (3 x + 1) e^-x is at most 1.6); its upper 32 bits, a signed number of half turns,
 // are rounded to fp32 (2^-25) and go to sincospif.  Integer arithmetic instead of fp64 products:
 // 75600 x 64 pairs took 74 us with those and take 14 (38.7 MB written, 6 us at the copy rate; the
 // rest is sincospif).  A thread keeps its pair and walks over the tokens.
