@@ -578,6 +578,7 @@ fp4_status_t fp4_dequantize_heads(fp4_fmt_t fmt, const uint8_t* codes, const uin
  *            (device) [T_kv][H_kv][D] with k_stride, v_stride; o_bf16 (device, out) [T_q][H][D] with
  *            o_stride.  Strides are at least a token's elements and multiples of 8 (slices of
  *            a fused projection do).  D 64 or 128; H a multiple of H_kv, at most 128 times it.
+ *            o may be q itself, and overlaps no key or value.
  *   scale    > 0 and below 1e30; softcap 0 (none) to 1e15 scale
  *   slopes   (device) fp32 [H] or NULL; q_pos: position of query row 0 on the keys' axis
  *   key_start, key_end  (device) int32 [T_q], or NULL for 0 and for T_kv (fp4_attn_ranges makes

@@ -296,6 +296,16 @@ def test_two_streams_at_once(fb):
     assert all(torch.equal(x, want[n]) for n in range(2) for x in got[n])
 
 
+@pytest.mark.parametrize("T_q,T_kv,H,H_kv", [(700, 300, 8, 2), (3, 5000, 8, 2), (130, 1, 3, 3)])
+def test_output_over_the_queries(fb, T_q, T_kv, H, H_kv):
+    import torch
+
+    q, k, v = randn(44, T_q, H, 128), randn(45, T_kv, H_kv, 128), randn(46, T_kv, H_kv, 128)
+    want = fb.attn_bf16(q, k, v, 0.1)
+    assert fb.attn_bf16(q, k, v, 0.1, o=q) is q
+    assert torch.equal(q, want)
+
+
 def test_helper_refusals(fb):
     import torch
 
