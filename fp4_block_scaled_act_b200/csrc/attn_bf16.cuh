@@ -63,7 +63,8 @@ struct AttnBfParams {
     bool heads_first;            // item order: key heads fastest, row tiles from the last (masked calls)
     float c;                     // scale log2(e), or (capped) scale / cap
     float cap;                   // capped: cap log2(e)
-    float tanh[6];               //   and the coefficients of tanh_near
+    float tanh[6];               //   the coefficients of tanh_near
+    float near;                  //   and the largest |q.k| it is for: cap / scale
     const float* slopes;         // [H] or null
     int64_t q_pos;               // position of query row 0 against key 0 (slopes)
     const int32_t* key_start;    // [T_q] or null (0)
@@ -167,10 +168,9 @@ FP4_DEV void attn_bf_fail(const AttnBfParams& p, volatile int* abort) {
     atomicCAS(p.status, 0, STATUS_TIMEOUT);
 }
 
-// The capped scores of one warp's tile where |s / cap| <= 1 for all of them: cap log2(e) tanh(s / cap)
-// as an odd polynomial s P(s^2), without a transcendental: tanh(x) = x sum_i t_i x^2i fitted here on
-// [0, 1] (minimax by reweighted least squares, degree 11, within 2^-21), the scale and the cap folded
-// into its coefficients on the host.
+// The capped score of |s / cap| <= 1: cap log2(e) tanh(s / cap) as an odd polynomial s P(s^2), without a
+// transcendental: tanh(x) = x sum_i t_i x^2i fitted here on [0, 1] (minimax by reweighted least squares,
+// degree 11, within 2^-21), the scale and the cap folded into its coefficients on the host.
 constexpr double AB_TANH[6] = {0x1.ffff96p-1, -0x1.553ce0p-2, 0x1.0f6ea4p-3, -0x1.a191d6p-5, 0x1.0803c2p-6, -0x1.742c92p-9};
 FP4_DEV uint64_t tanh_near(uint64_t s, const float (&t)[6]) {
     const uint64_t y = f2_mul(s, s);
@@ -584,8 +584,11 @@ __global__ void __launch_bounds__(AB_THREADS, 1)
 #pragma unroll
                         for (int y = 0; y < 32; y += 2)
                             far = fmaxf(fmaxf(far, fabsf(__uint_as_float(v[q][y]))), fabsf(__uint_as_float(v[q][y + 1])));
+                    // Each value takes the form of its own size.  The warp's vote, in which masked keys and other
+                    // rows take part, only skips the other form where no value takes it: one form a tile by that
+                    // vote made the far one 1.3 times as fast, but a row's bits then hung on what it does not see.
                     // (a NaN is passed over by the maximum and stays one in either form)
-                    if (__all_sync(0xffffffffu, far * p.c <= 1.0f)) {
+                    if (__all_sync(0xffffffffu, far <= p.near || tok < 0)) {
 #pragma unroll
                         for (int q = 0; q < 4; ++q)
 #pragma unroll
@@ -598,12 +601,18 @@ __global__ void __launch_bounds__(AB_THREADS, 1)
                     } else {
                         // tanh(x) = 1 - 2 / (1 + 2^(2 x log2 e)): within 2^-21 of cap
                         const float c2 = 2.0f * 1.44269504f * p.c;
+                        auto far_form = [&](float s) {
+                            return __fmaf_rn(-2.0f * p.cap, rcp_approx(1.0f + ex2(s * c2)), p.cap);
+                        };
 #pragma unroll
                         for (int q = 0; q < 4; ++q)
 #pragma unroll
-                            for (int y = 0; y < 32; ++y) {
-                                const float z = rcp_approx(1.0f + ex2(__uint_as_float(v[q][y]) * c2));
-                                v[q][y] = __float_as_uint(__fmaf_rn(-2.0f * p.cap, z, p.cap));
+                            for (int y = 0; y < 32; y += 2) {
+                                const float s0 = __uint_as_float(v[q][y]), s1 = __uint_as_float(v[q][y + 1]);
+                                float a, b;
+                                f2_unpack(tanh_near(f2_pack(s0, s1), p.tanh), a, b);
+                                v[q][y] = __float_as_uint(fabsf(s0) <= p.near ? a : far_form(s0));
+                                v[q][y + 1] = __float_as_uint(fabsf(s1) <= p.near ? b : far_form(s1));
                             }
                     }
                 }

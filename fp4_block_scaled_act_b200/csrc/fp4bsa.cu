@@ -1473,6 +1473,7 @@ fp4_status_t fp4_attn_bf16(const void* q_bf16, int64_t q_stride, int64_t T_q, co
     p.cap = (float)(softcap * log2e);
     if (softcap > 0.0f) {
         const double x = (double)scale / softcap;  // tanh's argument per unit of q.k
+        p.near = (float)((double)softcap / scale);
         double f = softcap * log2e * x;
         for (int i = 0; i < 6; ++i, f *= x * x) p.tanh[i] = (float)(AB_TANH[i] * f);
     }
