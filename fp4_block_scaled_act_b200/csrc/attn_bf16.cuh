@@ -170,8 +170,9 @@ FP4_DEV void attn_bf_fail(const AttnBfParams& p, volatile int* abort) {
 
 // The capped score of |s / cap| <= 1: cap log2(e) tanh(s / cap) as an odd polynomial s P(s^2), without a
 // transcendental: tanh(x) = x sum_i t_i x^2i fitted here on [0, 1] (minimax by reweighted least squares,
-// degree 11, within 2^-21), the scale and the cap folded into its coefficients on the host.
-constexpr double AB_TANH[6] = {0x1.ffff96p-1, -0x1.553ce0p-2, 0x1.0f6ea4p-3, -0x1.a191d6p-5, 0x1.0803c2p-6, -0x1.742c92p-9};
+// degree 11, within 2^-20.6 of its value: relative, so that small scores keep their accuracy under a large
+// cap), the scale and the cap folded into its coefficients on the host.
+constexpr double AB_TANH[6] = {0x1.ffffecp-1, -0x1.554a16p-2, 0x1.1000f6p-3, -0x1.a6c0f0p-5, 0x1.1251b4p-6, -0x1.92016cp-9};
 FP4_DEV uint64_t tanh_near(uint64_t s, const float (&t)[6]) {
     const uint64_t y = f2_mul(s, s);
     uint64_t e = f2_splat(t[5]);

@@ -102,3 +102,35 @@ def test_rows_that_are_not_there(fb, g, D):
         got.append(fb.attn_bf16(q, k, v, 0.1, softcap=30.0, return_lse=True))
     for o, lse in got[1:]:
         assert torch.equal(o, got[0][0]) and torch.equal(lse, got[0][1])
+
+
+@pytest.mark.parametrize("cap", [0.5, 30.0, 1e3, 1e5, 1e7])
+@pytest.mark.parametrize("T_q,T_kv,H,H_kv,D", [(1, 3000, 6, 2, 128), (130, 700, 3, 1, 64)])
+def test_small_scores_beside_large_ones(fb, cap, T_q, T_kv, H, H_kv, D):
+    """Every seventh key scores far below -cap (and has no weight): the others keep their accuracy."""
+    import torch
+
+    q, k, v = randn(10, T_q, H, D), randn(11, T_kv, H_kv, D), randn(12, T_kv, H_kv, D)
+    q[:, :, 0] = 1.0
+    k[:, :, 0] = 0.0
+    k[::7, :, 0] = -200.0 * cap
+    o, lse = fb.attn_bf16(q, k, v, 0.1, softcap=cap, return_lse=True)
+    check(o, lse, q, k, v, 0.1, cap)
+
+
+@pytest.mark.parametrize("cap", [1e-3, 1.0, 30.0, 1e6])
+def test_the_capped_score_itself(fb, cap):
+    """One key: lse is the capped score.  2^-20 of it, and 2^-22 for the two factors between log2 and log units
+    and the roundings around them (four of 2^-24)."""
+    import torch
+
+    T, D = 4000, 64
+    q, k = torch.zeros(T, 1, D, device="cuda"), torch.zeros(1, 1, D, device="cuda")
+    q[:, 0, 0] = torch.logspace(-6, 2, T, device="cuda") * cap * 8
+    q[::2] *= -1
+    k[0, 0, 0] = 1.0
+    q, k = q.bfloat16(), k.bfloat16()
+    _, lse = fb.attn_bf16(q, k, k, 0.125, softcap=cap, return_lse=True)
+    ref = cap * torch.tanh(q[:, 0, 0].double() * 0.125 / cap)
+    err = ((lse[:, 0].double() - ref) / ref).abs()
+    assert float(err.max()) <= 2.0 ** -20 + 2.0 ** -22
