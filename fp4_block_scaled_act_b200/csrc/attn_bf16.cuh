@@ -63,8 +63,7 @@ struct AttnBfParams {
     bool heads_first;            // item order: key heads fastest, row tiles from the last (masked calls)
     float c;                     // scale log2(e), or (capped) scale / cap
     float cap;                   // capped: cap log2(e)
-    float tanh[6];               //   the coefficients of tanh_near
-    float near;                  //   and the largest |q.k| it is for: cap / scale
+    float tanh[6];               //   and the coefficients of tanh_near
     const float* slopes;         // [H] or null
     int64_t q_pos;               // position of query row 0 against key 0 (slopes)
     const int32_t* key_start;    // [T_q] or null (0)
@@ -168,17 +167,19 @@ FP4_DEV void attn_bf_fail(const AttnBfParams& p, volatile int* abort) {
     atomicCAS(p.status, 0, STATUS_TIMEOUT);
 }
 
-// The capped score of |s / cap| <= 1: cap log2(e) tanh(s / cap) as an odd polynomial s P(s^2), without a
-// transcendental: tanh(x) = x sum_i t_i x^2i fitted here on [0, 1] (minimax by reweighted least squares,
+// The capped score of |s / cap| <= 1: cap log2(e) tanh(x), x = s / cap, as an odd polynomial x P(x^2), without
+// a transcendental: tanh(x) = x sum_i t_i x^2i fitted here on [0, 1] (minimax by reweighted least squares,
 // degree 11, within 2^-20.6 of its value: relative, so that small scores keep their accuracy under a large
-// cap), the scale and the cap folded into its coefficients on the host.
+// cap), cap log2(e) folded into its coefficients on the host.  Folding the scale in too would save the product
+// s / cap, 4 % of the time, but its powers overflow fp32 for small caps and underflow for large ones (2 %
+// of the score at a cap of 1e6 times the scale).
 constexpr double AB_TANH[6] = {0x1.ffffecp-1, -0x1.554a16p-2, 0x1.1000f6p-3, -0x1.a6c0f0p-5, 0x1.1251b4p-6, -0x1.92016cp-9};
-FP4_DEV uint64_t tanh_near(uint64_t s, const float (&t)[6]) {
-    const uint64_t y = f2_mul(s, s);
+FP4_DEV uint64_t tanh_near(uint64_t x, const float (&t)[6]) {
+    const uint64_t y = f2_mul(x, x);
     uint64_t e = f2_splat(t[5]);
 #pragma unroll
     for (int i = 4; i >= 0; --i) e = f2_fma(e, y, f2_splat(t[i]));
-    return f2_mul(s, e);
+    return f2_mul(x, e);
 }
 
 // An item as the planner gives it to the other warps
@@ -589,31 +590,32 @@ __global__ void __launch_bounds__(AB_THREADS, 1)
                     // rows take part, only skips the other form where no value takes it: one form a tile by that
                     // vote made the far one 1.3 times as fast, but a row's bits then hung on what it does not see.
                     // (a NaN is passed over by the maximum and stays one in either form)
-                    if (__all_sync(0xffffffffu, far <= p.near || tok < 0)) {
+                    const uint64_t cc = f2_splat(p.c);
+                    if (__all_sync(0xffffffffu, far * p.c <= 1.0f || tok < 0)) {
 #pragma unroll
                         for (int q = 0; q < 4; ++q)
 #pragma unroll
                             for (int y = 0; y < 32; y += 2) {
+                                const uint64_t x = f2_mul(f2_pack(__uint_as_float(v[q][y]), __uint_as_float(v[q][y + 1])), cc);
                                 float a, b;
-                                f2_unpack(tanh_near(f2_pack(__uint_as_float(v[q][y]), __uint_as_float(v[q][y + 1])), p.tanh),
-                                          a, b);
+                                f2_unpack(tanh_near(x, p.tanh), a, b);
                                 v[q][y] = __float_as_uint(a), v[q][y + 1] = __float_as_uint(b);
                             }
                     } else {
                         // tanh(x) = 1 - 2 / (1 + 2^(2 x log2 e)): within 2^-21 of cap
-                        const float c2 = 2.0f * 1.44269504f * p.c;
-                        auto far_form = [&](float s) {
-                            return __fmaf_rn(-2.0f * p.cap, rcp_approx(1.0f + ex2(s * c2)), p.cap);
+                        auto far_form = [&](float x) {
+                            return __fmaf_rn(-2.0f * p.cap, rcp_approx(1.0f + ex2(x * (2.0f * 1.44269504f))), p.cap);
                         };
 #pragma unroll
                         for (int q = 0; q < 4; ++q)
 #pragma unroll
                             for (int y = 0; y < 32; y += 2) {
-                                const float s0 = __uint_as_float(v[q][y]), s1 = __uint_as_float(v[q][y + 1]);
-                                float a, b;
-                                f2_unpack(tanh_near(f2_pack(s0, s1), p.tanh), a, b);
-                                v[q][y] = __float_as_uint(fabsf(s0) <= p.near ? a : far_form(s0));
-                                v[q][y + 1] = __float_as_uint(fabsf(s1) <= p.near ? b : far_form(s1));
+                                const uint64_t x = f2_mul(f2_pack(__uint_as_float(v[q][y]), __uint_as_float(v[q][y + 1])), cc);
+                                float x0, x1, a, b;
+                                f2_unpack(x, x0, x1);
+                                f2_unpack(tanh_near(x, p.tanh), a, b);
+                                v[q][y] = __float_as_uint(fabsf(x0) <= 1.0f ? a : far_form(x0));
+                                v[q][y + 1] = __float_as_uint(fabsf(x1) <= 1.0f ? b : far_form(x1));
                             }
                     }
                 }

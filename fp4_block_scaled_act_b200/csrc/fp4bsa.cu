@@ -1469,14 +1469,10 @@ fp4_status_t fp4_attn_bf16(const void* q_bf16, int64_t q_stride, int64_t T_q, co
     // then stay in L2
     p.heads_first = key_start || key_end;
     const double log2e = 1.4426950408889634;
-    p.c = (float)(softcap > 0.0f ? (double)scale / softcap : scale * log2e);
+    // (a cap that is 1e-38 of the scale and less: every score but zero is beyond it)
+    p.c = (float)(softcap > 0.0f ? std::min((double)scale / softcap, 3.0e38) : scale * log2e);
     p.cap = (float)(softcap * log2e);
-    if (softcap > 0.0f) {
-        const double x = (double)scale / softcap;  // tanh's argument per unit of q.k
-        p.near = (float)((double)softcap / scale);
-        double f = softcap * log2e * x;
-        for (int i = 0; i < 6; ++i, f *= x * x) p.tanh[i] = (float)(AB_TANH[i] * f);
-    }
+    for (int i = 0; i < 6; ++i) p.tanh[i] = (float)(AB_TANH[i] * (softcap * log2e));
     p.slopes = slopes, p.q_pos = q_pos, p.key_start = key_start, p.key_end = key_end;
     p.v = static_cast<const __nv_bfloat16*>(v_bf16), p.v_stride = v_stride;
     p.o = static_cast<__nv_bfloat16*>(o_bf16), p.o_stride = o_stride, p.lse = lse;
