@@ -182,6 +182,27 @@ FP4_DEV uint64_t tanh_near(uint64_t x, const float (&t)[6]) {
     return f2_mul(x, e);
 }
 
+// Distance bias.  A query may stand far from the keys of its range ks .. ke - 1, where fp32 holds neither its
+// distances (beyond 2^24) nor their differences in a large bias.  Keys are therefore counted from `pos`, the
+// query's own place if that is within the range, else the range's nearest key: |q_pos + i - j| is |pos - j| and a
+// part that all keys share.  The latter cancels in o and is added to lse.  A slope below 0 makes far keys the
+// heavy ones; for those distances are taken less the largest (`far`), so that biases are 0 at the heaviest key.
+struct AttnBfBias {
+    int pos;
+    float slope, far;  // bias in log2 units: (|pos - j| - far) slope
+    FP4_DEV AttnBfBias(const AttnBfParams& p, int tok, int head, int ks, int ke) {
+        const int64_t at = p.q_pos + tok;
+        pos = (int)(at < ks ? ks : at >= ke ? ke - 1 : at);
+        slope = -1.44269504f * p.slopes[head];
+        far = slope > 0.0f ? (float)max(pos - ks, ke - 1 - pos) : 0.0f;
+    }
+    // lse of biases as above, to that of the whole distances
+    FP4_DEV float lse(const AttnBfParams& p, int tok, int head, float log2_sum) const {
+        const int64_t apart = p.q_pos + tok - pos;
+        return (log2_sum + far * slope) * 0.693147181f - p.slopes[head] * fabsf((float)apart);
+    }
+};
+
 // An item as the planner gives it to the other warps
 struct AttnBfItem {
     int t0, hk, z, subs; // first token, key head, part; row tiles
@@ -550,7 +571,12 @@ __global__ void __launch_bounds__(AB_THREADS, 1)
             const int all_lo = __reduce_max_sync(0xffffffffu, ks), all_hi = __reduce_min_sync(0xffffffffu, ke);
             const int jb = info[e].jb, n = w < info[e].subs ? tiles_of(info[e].n, w) : 0;
             float m = -INFINITY, l = 0.0f;  // the maximum that P and O refer to (log2 units), the sum
-            const float slope = BIAS && tok >= 0 ? -1.44269504f * p.slopes[head] : 0.0f;
+            int bias_pos = 0;
+            float slope = 0.0f, bias_far = 0.0f;
+            if (BIAS && tok >= 0) {
+                const AttnBfBias b(p, tok, head, ks, ke);
+                bias_pos = b.pos, slope = b.slope, bias_far = b.far;
+            }
             for (int i = 0; ok && i < n; ++i, ++ns) {
                 ok = mbar_wait_warp(&s_full[w], ns & 1u, p.timeout_ns, abort);
                 if (!ok) break;
@@ -620,14 +646,31 @@ __global__ void __launch_bounds__(AB_THREADS, 1)
                     }
                 }
                 if (BIAS) {
-                    const float from = (float)(p.q_pos + tok - k0);
+                    const float from = (float)(bias_pos - k0);
+                    if (!CAP) {
+                        const float off = -bias_far * slope;
 #pragma unroll
-                    for (int q = 0; q < 4; ++q)
+                        for (int q = 0; q < 4; ++q)
 #pragma unroll
-                        for (int y = 0; y < 32; ++y) {
-                            const float b = fabsf(from - (float)(32 * q + y)) * slope, s = __uint_as_float(v[q][y]);
-                            v[q][y] = __float_as_uint(CAP ? s + b : __fmaf_rn(s, p.c, b));
-                        }
+                            for (int y = 0; y < 32; ++y) {
+                                const float b = __fmaf_rn(fabsf(from - (float)(32 * q + y)), slope, off);
+                                v[q][y] = __float_as_uint(__fmaf_rn(__uint_as_float(v[q][y]), p.c, b));
+                            }
+                    } else if (__any_sync(0xffffffffu, bias_far != 0.0f)) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+#pragma unroll
+                            for (int y = 0; y < 32; ++y)
+                                v[q][y] = __float_as_uint(__fmaf_rn(fabsf(from - (float)(32 * q + y)) - bias_far, slope,
+                                                                    __uint_as_float(v[q][y])));
+                    } else {  // (the same where nothing is taken off)
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+#pragma unroll
+                            for (int y = 0; y < 32; ++y)
+                                v[q][y] = __float_as_uint(__fmaf_rn(fabsf(from - (float)(32 * q + y)), slope,
+                                                                    __uint_as_float(v[q][y])));
+                    }
                 }
                 // the multiplier still to be applied
                 const float c = CAP || BIAS ? 1.0f : p.c;
@@ -767,8 +810,11 @@ __global__ void __launch_bounds__(AB_THREADS, 1)
             if (tok >= 0) {
                 if (p.parts > 1)
                     p.part_ml[part] = some ? make_float2(m, l) : make_float2(-INFINITY, 0.0f);
+                else if (p.lse && !some)
+                    p.lse[row] = -INFINITY;
                 else if (p.lse)
-                    p.lse[row] = some ? (m + log2f(l)) * 0.693147181f : -INFINITY;
+                    p.lse[row] = BIAS ? AttnBfBias(p, tok, head, ks, ke).lse(p, tok, head, m + log2f(l))
+                                      : (m + log2f(l)) * 0.693147181f;
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&item_empty[e]);
@@ -813,7 +859,16 @@ __global__ void __launch_bounds__(128) attn_bf16_join_kernel(const __grid_consta
     for (int e = 0; e < V; e += 2)
         *reinterpret_cast<__nv_bfloat162*>(dst + e) =
             some ? __floats2bfloat162_rn(acc[e] / l, acc[e + 1] / l) : __floats2bfloat162_rn(0.0f, 0.0f);
-    if (p.lse && lane == 0) p.lse[row] = some ? (m + log2f(l)) * 0.693147181f : -INFINITY;
+    if (p.lse && lane == 0) {
+        float y = some ? (m + log2f(l)) * 0.693147181f : -INFINITY;
+        if (some && p.slopes) {
+            const int ks = p.key_start ? max(p.key_start[tok], 0) : 0;
+            const int ke = p.key_end ? min(p.key_end[tok], p.T_kv) : p.T_kv;
+            const int head = (int)(row - tok * p.H);
+            y = AttnBfBias(p, (int)tok, head, ks, ke).lse(p, (int)tok, head, m + log2f(l));
+        }
+        p.lse[row] = y;
+    }
 }
 
 // Key ranges of query rows of packed documents: row i of document d (q_offsets[d] <= i <

@@ -580,7 +580,10 @@ fp4_status_t fp4_dequantize_heads(fp4_fmt_t fmt, const uint8_t* codes, const uin
  *            a fused projection do).  D 64 or 128; H a multiple of H_kv, at most 128 times it.
  *            o may be q itself, and overlaps no key or value.
  *   scale    > 0 and below 1e30; softcap 0 (none) to 1e15 scale
- *   slopes   (device) fp32 [H] or NULL; q_pos: position of query row 0 on the keys' axis
+ *   slopes   (device) fp32 [H] or NULL; q_pos: position of query row 0 on the keys' axis, below 2^40 in
+ *            magnitude.  Distances are whole numbers; beyond the smallest one of a row's keys (the
+ *            largest, where the slope is negative) they are rounded to 24 bits, and what all the
+ *            row's keys share enters lse alone
  *   key_start, key_end  (device) int32 [T_q], or NULL for 0 and for T_kv (fp4_attn_ranges makes
  *            them for documents, causal order and prefixes)
  *   lse      (device, out) fp32 [T_q][H], or NULL
