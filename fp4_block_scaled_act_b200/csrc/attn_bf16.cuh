@@ -76,7 +76,7 @@ struct AttnBfParams {
     float* lse;                  // [T_q][H] or null
     int parts;                   // splits, or twice that (alt); > 1: partial results
     float* part_o;               //   [parts][T_q H][D]
-    float2* part_ml;             //   [parts][T_q H] (maximum in log2 units, sum)
+    float2* part_ml;             //   [parts][T_q H] (maximum in log2 units, sum; -1: no keys)
     uint64_t timeout_ns;
     int* status;
 };
@@ -809,7 +809,7 @@ __global__ void __launch_bounds__(AB_THREADS, 1)
             }
             if (tok >= 0) {
                 if (p.parts > 1)
-                    p.part_ml[part] = some ? make_float2(m, l) : make_float2(-INFINITY, 0.0f);
+                    p.part_ml[part] = some ? make_float2(m, l) : make_float2(-INFINITY, -1.0f);
                 else if (p.lse && !some)
                     p.lse[row] = -INFINITY;
                 else if (p.lse)
@@ -830,7 +830,7 @@ __global__ void __launch_bounds__(AB_THREADS, 1)
 }
 
 // The parts of a row joined in order: o = sum_z 2^(m_z - m) O_z / sum_z 2^(m_z - m) l_z.  A part without
-// keys (l = 0) is passed over.  A warp takes a row, D / 32 values a lane.
+// keys (l < 0) is passed over; where all keys score -infinity (m too, l = 0) the division gives NaN, as in one part.  A warp takes a row, D / 32 values a lane.
 template <int D>
 __global__ void __launch_bounds__(128) attn_bf16_join_kernel(const __grid_constant__ AttnBfParams p) {
     constexpr int V = D / 32;
@@ -845,9 +845,9 @@ __global__ void __launch_bounds__(128) attn_bf16_join_kernel(const __grid_consta
     bool some = false;
     for (int z = 0; z < p.parts; ++z) {
         const float2 ml = p.part_ml[z * rows + row];
-        if (ml.y == 0.0f) continue;
+        if (ml.y < 0.0f) continue;
         some = true;
-        const float f = exp2f(ml.x - m);
+        const float f = ml.x == m ? 1.0f : exp2f(ml.x - m);
         l += ml.y * f;
         const float* src = p.part_o + (z * rows + row) * D + lane * V;
 #pragma unroll

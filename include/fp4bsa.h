@@ -572,7 +572,8 @@ fp4_status_t fp4_dequantize_heads(fp4_fmt_t fmt, const uint8_t* codes, const uin
  *   slopes:  s_ij -= slopes[h] |q_pos + i - j|;
  *   o_i = sum_j p_ij v_j / sum_j p_ij with p_ij = exp(s_ij - max_j s_ij) over the keys
  *   key_start[i] <= j < key_end[i] (cut to 0 .. T_kv), lse_i = log sum_j exp(s_ij).
- * A row that sees no key gives o = 0 and lse = -infinity.  A row's result depends on no key or
+ * A row that sees no key gives o = 0 and lse = -infinity, one whose keys all score -infinity o = NaN
+ * and lse = -infinity.  A row's result depends on no key or
  * value outside its range, whatever these hold (infinities and NaN among them).
  *   q_bf16   (device) [T_q][H][D] bf16, q_stride elements from token to token; k_bf16, v_bf16
  *            (device) [T_kv][H_kv][D] with k_stride, v_stride; o_bf16 (device, out) [T_q][H][D] with
