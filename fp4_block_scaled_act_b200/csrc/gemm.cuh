@@ -932,7 +932,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Gemm2Cfg<KIND>::THRE
                         if (with_res) {
                             // tile 0 is loaded twice for every output tile, tiles 1 and 2 once
                             const uint32_t parity = k % 3 == 0 ? (k == 3 ? 1u : 0u) : res_tiles & 1u;
-                            const bool loaded = mbar_wait(&res_full[3 * ew + k % 3], parity, p.timeout_ns, abort);
+                            // (the abort flag does not end this wait: a copy in flight lands before its tile is written,
+                            // its barrier armed again or the CTA exits)
+                            const bool loaded = mbar_wait_drain(&res_full[3 * ew + k % 3], parity, p.timeout_ns);
                             if (!__all_sync(0xffffffffu, loaded) && lane == 0) gemm2_fail(p, abort, peer_abort);
                         } else {
                             // the last store from this tile: the newest for chunk 0 (the chunk 3 before), else
