@@ -243,7 +243,8 @@ typedef enum {
     FP4_ACT_NONE = 0,
     FP4_ACT_GELU_TANH = 1, /* as above, not rounded to bf16 */
     FP4_ACT_SILU = 2       /* z / (1 + exp(-z)) */
-    /* both evaluated in fp32 as z / (1 + 2^t) within (2 |t| + 8) 2^-23 of their value and 2^-126 */
+    /* both evaluated in fp32 as z / (1 + 2^t): within (2 |t| + 8) 2^-23 of their value, or within
+     * |z| 2^-126 where 1 / (1 + 2^t) is below 2^-126 (it is 0 there: SiLU from z = -87.4 down) */
 } fp4_act_t;
 
 /* A block's output projection with what follows it (Wan2.2 blocks: x + proj(h) * gate, the gate
