@@ -11,7 +11,8 @@
 // that bf16, gives the codes and scales that the head quantizer gives for the bf16 form's output,
 // and neither depends on how the fp32 arithmetic in between is ordered.  The sum of squares is
 // taken in fp32 for eight elements at a time (their squares are exact there) and in fp64 above
-// that: four roundings of positive terms, so the root is within a relative 2^-23 in every case.
+// that: four roundings of positive terms, so the root is within a relative 2^-23.  Where squares leave
+// fp32's range (seen from the root) they are summed in fp64, and all pairs are rotated in fp64.
 //
 // What bounds it: instructions.  75600 tokens of 40 + 40 heads of 128 move 3.1 GB in the bf16 form, 477 us
 // at the copy rate, and take 614 (5.0 TB/s); with NVFP4 out 2.0 GB, 302 us, and 760, at 385 warp
@@ -224,6 +225,11 @@ __global__ void __launch_bounds__(NR_THREADS, 5)
             f = __ldg(reinterpret_cast<const float4*>(row + (c < 2 ? c0 : c1 - 8) + 4 * c));
         cs[c] = f2_pack(f.x, f.z), sn[c] = f2_pack(f.y, f.w);
     }
+    // r is plain within 2^+-40: squares were then no subnormals and did not overflow, and r in fp32 is good.
+    // Elsewhere the norm is taken again in fp64, and all pairs are rotated in fp64 (low_high's bound needs
+    // products that are no subnormals and do not overflow).
+    constexpr uint32_t PLAIN_FROM = (127 - 40) << 23, PLAIN_SPAN = 80 << 23;
+    auto plain = [](double r) { return __float_as_uint((float)r) - PLAIN_FROM < PLAIN_SPAN; };
     cp_async_wait_all();
     // a unit's sum of squares: eight squares at a time in fp32, the rest in fp64
     auto squares = [](const uint32_t (&x)[8]) {
@@ -243,6 +249,17 @@ __global__ void __launch_bounds__(NR_THREADS, 5)
         }
         return sum;
     };
+    auto squares_fp64 = [&](int i) {
+        const uint32_t* x = reinterpret_cast<const uint32_t*>(mine_at + i * 64);
+        double sum = 0.0;
+#pragma unroll 1
+        for (int k = 0; k < 8; ++k) {
+            const uint32_t w = x[k < 4 ? k : 32 * 4 + k - 4];
+            const double a = bf16_lo(w), b = bf16_hi(w);
+            sum += a * a + b * b;
+        }
+        return sum;
+    };
     auto unit = [&](int i, uint32_t (&x)[8]) {
         const uint4 a = mine_at[i * 64], b = mine_at[i * 64 + 32];
         x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
@@ -256,6 +273,11 @@ __global__ void __launch_bounds__(NR_THREADS, 5)
                 unit(i, x);
                 sum += squares(x);
             }
+        // a lane whose sum is not within 2^-90 .. 2^120 takes it again in fp64, before the token's lanes meet
+        if (real && (uint32_t)__double2hiint(sum) - ((1023 - 90) << 20) >= (210 << 20)) {
+            sum = 0.0;
+            for (int i = 0; first + i * stride < units; ++i) sum += squares_fp64(i);
+        }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         if (wpt > 1) {  // the token's warps in order
@@ -264,7 +286,9 @@ __global__ void __launch_bounds__(NR_THREADS, 5)
             sum = 0.0;
             for (int k = 0; k < wpt; ++k) sum += red[warp / wpt * wpt + k];
         }
-        r = rsqrt_fp64(sum / (double)(q.H * D) + (double)p.eps);
+        const double m = sum / (double)(q.H * D) + (double)p.eps;
+        r = rsqrt_fp64(m);
+        if (!plain(r)) r = 1.0 / sqrt(m);
     }
     if (t >= rows) return;
     // r c, r s and -r s: once a token, or once a head's unit
@@ -274,7 +298,8 @@ __global__ void __launch_bounds__(NR_THREADS, 5)
 #pragma unroll
         for (int k = 0; k < 4; ++k) cr[k] = f2_mul(cs[k], r2), sr[k] = f2_mul(sn[k], r2), nr[k] = f2_mul(sn[k], m2);
     };
-    if (TOKEN) scale_table();
+    uint32_t all = 0u;  // the pairs to be taken in fp64 whatever their values
+    if (TOKEN) scale_table(), all = plain(r) ? 0u : 0xFFu;
 
     constexpr int G = OUT == NR_NVFP4 ? 16 : 32;  // FP4: elements a scale
     constexpr int APR = OUT == NR_NVFP4 ? 2 : 1;  // and scale atoms per 128 tokens of a head
@@ -321,7 +346,17 @@ __global__ void __launch_bounds__(NR_THREADS, 5)
             for (int o = LPH / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
             r = rsqrt_fp64(sum * (1.0 / D) + (double)p.eps);
         }
-        if (!TOKEN) scale_table();
+        if (!TOKEN) {
+            all = 0u;  // (without a norm r is 1)
+            if (__any_sync(0xffffffffu, !plain(r))) {
+                all = plain(r) ? 0u : 0xFFu;
+                double sum = squares_fp64(i);
+#pragma unroll
+                for (int o = LPH / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                if (all) r = 1.0 / sqrt(sum * (1.0 / D) + (double)p.eps);
+            }
+            scale_table();
+        }
         const float* const wp = weight ? weight + (TOKEN && mine ? h * D : 0) : nullptr;
         // Rotation pairs j = 2k and 2k + 1 are (a, b), times their weights.  In memory order their four
         // values are a b a b (interleaved), or the two a's in chunk 0 and the two b's in chunk 1 (half).
@@ -369,7 +404,7 @@ __global__ void __launch_bounds__(NR_THREADS, 5)
         }
 
         // the unit's sixteen values as bf16, y[k] in memory order: chunk 0, then chunk 1
-        uint32_t y[8], again = 0u;
+        uint32_t y[8], again = all;
 #pragma unroll
         for (int k = 0; k < 4; ++k)
             again |= low_high<HALF>(a[k], b[k], y[HALF ? k : 2 * k], y[HALF ? 4 + k : 2 * k + 1]) << (2 * k);

@@ -530,14 +530,16 @@ typedef enum {
 /* RMS norm and rotation of queries and keys in one pass over them:
  *   y = x w / sqrt(mean(x^2) + eps), then each pair (u, v) of the head's first `rot` elements
  *   becomes (u c - v s, u s + v c); the output is the nearest bf16 of that real number (of one
- *   within 2^-24 of it, the error of the root).
+ *   within 2^-24 of it, the error of the root; below 2^-80 within 2^-80).
  *   q_bf16, k_bf16  (device) [T][H][D] bf16, q_stride / k_stride elements from token to token
  *                   (>= H D, a multiple of 8: slices of a fused projection do); heads are
  *                   contiguous.  k_bf16 and k_out NULL: queries alone.  D 64 or 128,
  *                   H D <= 16384.
- *   q_weight, k_weight  (device) fp32, 16-byte aligned, or NULL for ones
- *   eps             >= 0; |x| below 2^62 (squares are summed from fp32 pairs)
- *   table           (device) fp32 [T][rot] (cos, sin) pairs, e.g. fp4_rope_table's; NULL with rot = 0
+ *   q_weight, k_weight  (device) fp32, below 2^80 in magnitude, 16-byte aligned, or NULL for ones
+ *   eps             >= 0; rows of any size (all zeros with an eps of 0: NaN, as 0 / 0; an infinity
+ *                   makes the finite values under its norm 0)
+ *   table           (device) fp32 [T][rot] (cos, sin) pairs, e.g. fp4_rope_table's, of a size
+ *                   (amplitude) within 2^-20 .. 2^20; NULL with rot = 0
  *   rot             rotated elements of each head, a multiple of 16, at most D
  *   q_out, k_out    (device, out) bf16, strides as above; q_out may be q_bf16 itself with the
  *                   same stride (likewise k), other overlaps are not allowed */
