@@ -530,7 +530,7 @@ typedef enum {
 /* RMS norm and rotation of queries and keys in one pass over them:
  *   y = x w / sqrt(mean(x^2) + eps), then each pair (u, v) of the head's first `rot` elements
  *   becomes (u c - v s, u s + v c); the output is the nearest bf16 of that real number (of one
- *   within 2^-24 of it, the error of the root; below 2^-80 within 2^-80).
+ *   within 2^-23 of it, the error of the root; below 2^-80 within 2^-80).
  *   q_bf16, k_bf16  (device) [T][H][D] bf16, q_stride / k_stride elements from token to token
  *                   (>= H D, a multiple of 8: slices of a fused projection do); heads are
  *                   contiguous.  k_bf16 and k_out NULL: queries alone.  D 64 or 128,
