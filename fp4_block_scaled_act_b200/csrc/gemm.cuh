@@ -1376,17 +1376,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Gemm2Cfg<KIND>::THRE
             // Waits, in the MMA warp's order, for everything a stage needs (the accumulator
             // and the overlap at a tile's first stage; A/B bytes of both CTAs; both CTAs'
             // scale buffer) and then releases the stage with named barrier 1 + it % TB.  After
-            // a failure it still releases the remaining stages of that tile without waiting,
-            // so the MMA warp, which checks the abort flag at the end of each tile, never
-            // waits on a barrier that nobody arrives at.  The ring of TB barrier ids cannot be lapped:
-            // the scale buffer of stage it + TB is free only after the MMA warp has passed
-            // stage it.
+            // a failure it still releases the remaining stages of that tile without waiting for their
+            // data, so the MMA warp, which checks the abort flag at the end of each tile, never
+            // waits on a barrier that nobody arrives at.  The ring of TB barrier ids must not be lapped
+            // (two arrivals of this warp would complete a barrier that the MMA warp then waits at for
+            // good): the scale buffer of stage it + TB is free only after the MMA warp has passed
+            // stage it, and after a failure, when scale buffers are no longer waited for, this warp waits for
+            // those MMAs itself.  It stops where they do not come: the MMA warp left after an earlier tile.
             if (rank == 0) {
                 uint32_t it = 0;
                 int tcount = 0;
                 bool ok = true;
                 Sched sc = sched0;
                 sc.begin();
+                const uint64_t mma_limit = p.timeout_ns > 100000000ull ? p.timeout_ns : 100000000ull;
                 int tile, kb0, kb1;
                 for (; ok && sc.get(tile, kb0, kb1); sc.step(kb0, kb1), ++tcount) {
                     const int b = tcount & 1;
@@ -1400,6 +1403,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Gemm2Cfg<KIND>::THRE
                         if (!got && ok) {
                             if (lane == 0) gemm2_fail(p, abort, peer_abort);
                             ok = false;
+                        }
+                        if (!ok && it >= TB) {
+                            const bool passed = mbar_wait_drain(&empty[(it - TB) % S], ((it - TB) / S) & 1u, mma_limit);
+                            if (!__all_sync(0xffffffffu, passed)) break;
                         }
                         __syncwarp();
                         named_bar_arrive(1u + it % TB, 64u);
