@@ -19,26 +19,38 @@
 // S into registers and writes P = 2^(s c - m) in bf16 over S in TMEM, in two halves of 64 keys, each
 // handed to the MMA warp as it is done; the fp32 weights (before rounding) are added to its sum.
 // O += P V with P as the TMEM operand, the first half while the second is being made, then the
-// next S.  m is a running reference, not the row's maximum: it is replaced only when the maximum has
-// grown past it by more than 2^8 (P then stays below 2^8, O and the sum far below overflow); only then
-// O is rescaled in TMEM, by the softmax warps, which know from S's arrival that the last P V is done.
+// next S.  m is a running reference, not the row's maximum (lazy rescaling, a published method of
+// streaming attention): it is replaced only when the maximum has grown past it by more than 2^8 (P then
+// stays below 2^8, the sum below 2^38, O within it for values below 2^88); only then O is rescaled in TMEM,
+// by the softmax warps, which know from S's arrival that the last P V is done.
 // What bounds it: per 128 x 128 scores 512 cycles of MMA for S and for P V each (head_dim 128), and
 // 16384 exponentials at 16 a cycle, 1024 cycles, in turn for a row tile, in parallel for the two.
 // Measured, head_dim 128: 8192 rows x 8192 keys x 16 heads 553 us (994 TFLOP/s, 0.60 of the library
-// GEMM's rate), causal 283 (972), capped 807, with a bias 708; head_dim 64 507.  The tensor pipe is
-// busy 0.54 of the cycles, the exponentials' pipe as much: what is left is each row tile's chain from
-// S over its maximum and exponentials to P V, which the other tile covers only in part.  Tried and no
+// GEMM's rate), causal 277 (993), capped 841 (1400 where tiles hold scores beyond the cap), with a bias
+// 729, both 1098; head_dim 64 494.  An SM that works has its tensor pipe busy 0.53 of the cycles, the
+// exponentials' pipe as much.  Part of the rest is the schedule: items go to the CTAs in a fixed order,
+// and 512 equal ones on 148 CTAs make a last round that is half empty (256 key tiles on the longest CTA,
+// 221 in the mean).  The rest is each row tile's chain from S over its maximum and exponentials to P V,
+// which the other tile covers only in part.  Tried and no
 // faster: 64-key tiles, a reference maximum guessed ahead, exponentials by polynomial for a share of
 // the keys, P handed over whole, a second MMA warp, O staged through shared memory.
-// Few keys: 32760 rows x 40 heads over 512 keys 423 us, over 256 281 (104 us of bytes): an item of
+// The kernels spill 100 to 300 bytes a thread (136 bytes of loads in the plain one, 356 MB a call above,
+// out of L1); a split of 56 / 224 registers would spill less and has not been timed.
+// Documents: an item has one key range for both its row tiles, and its length does not decide where it
+// runs.  Three clips of 4290 tokens x 24 heads, 179 us: 54 key tiles on the longest CTA, 37 in the mean, 34
+// if each row tile took its own range.
+// Few keys: 32760 rows x 40 heads over 512 keys 420 us, over 256 281 (104 us of bytes): an item of
 // one key tile takes a softmax warp some 7000 cycles in turn, most of it the wait for S, its
-// exponentials, the wait for P V, and reading and storing O.  One token x 40 heads (8 key heads) over 100001 keys: 94 us (62 of bytes).
+// exponentials, the wait for P V, and reading and storing O.  One token x 40 heads (8 key heads) over 100001
+// keys: 107 us (62 of bytes).
 //
 // Masks cost only where they cut: tiles outside every row's range are not visited, a warp whose
 // 32 rows see a whole tile does not test keys.  Within a tile that some row does not see whole,
 // a value of V that is infinite or NaN would reach rows that exclude its key (0 * inf in P V):
 // the V guard looks through such tiles in shared memory, puts zeros in place of such values, and
-// the rows that do attend them get them added at the end (rare and slow, see `repair`).
+// the rows that do attend them get them added at the end (`repair`).  That is slow, also where no row
+// attends them: one token over 100001 keys 112 us with zeros behind the last key and 167 with NaN there, over
+// 1000 keys 30 and 185; 8192 rows x 8100 keys 569 and 918.
 //
 // With few row tiles the key tiles are split into parts, each an item of its own; each part
 // writes its unnormalized O, maximum and sum, and a second kernel joins them in a fixed order.

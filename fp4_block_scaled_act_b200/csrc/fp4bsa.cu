@@ -1438,7 +1438,7 @@ fp4_status_t fp4_attn_bf16(const void* q_bf16, int64_t q_stride, int64_t T_q, co
                            size_t ws_bytes, void* stream) {
     if (!q_bf16 || !k_bf16 || !v_bf16 || !o_bf16) return FP4_ERR_INVALID_ARG;
     if (!(scale > 0.0f) || !(scale < 1.0e30f) || !(softcap >= 0.0f) || !(softcap <= 1.0e15f * scale))
-        return FP4_ERR_INVALID_ARG;  // (beyond, squares of scores in reach of the cap overflow)
+        return FP4_ERR_INVALID_ARG;
     if (q_pos <= -((int64_t)1 << 40) || q_pos >= ((int64_t)1 << 40)) return FP4_ERR_INVALID_ARG;
     fp4_status_t s = check_attn_bf16(T_q, T_kv, H, H_kv, D);
     if (s != FP4_OK) return s;

@@ -15,9 +15,10 @@
 // fp32's range (seen from the root) they are summed in fp64, and all pairs are rotated in fp64.
 //
 // What bounds it: instructions.  75600 tokens of 40 + 40 heads of 128 move 3.1 GB in the bf16 form, 477 us
-// at the copy rate, and take 614 (5.0 TB/s); with NVFP4 out 2.0 GB, 302 us, and 760, at 385 warp
-// instructions for 512 elements and 0.65 of the issue slots.  Of those 385 the fp64 path of the
-// pairs that fp32 leaves open takes some 80, quantization 90, the sum of squares 26, the rotation 16.
+// at the copy rate, and take 622 (5.0 TB/s); with NVFP4 out 2.0 GB, 302 us, and 790, at 395 warp
+// instructions for 512 elements and 0.65 of the issue slots.  Of those 395 the fp64 path of the
+// pairs that fp32 leaves open takes some 80 (and finding them, low_high, comes on top), quantization 90, the
+// sum of squares 26, the rotation 16, the check that the root is one for fp32 some 10.
 // What was taken out: the root goes into the table's entries, once a token instead of once a weight;
 // pairs of pairs are rotated in packed fp32; scale bytes are stored one by one instead of gathered by
 // shuffles; the interleaved layout multiplies its weights singly, since packed products would
@@ -43,12 +44,13 @@ struct RopeFreqs {
 };
 
 // table[t][j] = amplitude (cos, sin)(2 pi frac(p turns_j)).  The fraction of the turn count is
-// the low 64 bits of the integer product, within 2^-34 of a turn for every position (turns_j is
-// within 2^-65, |p| at most 2^31, and the host's frequency e^-x within (3 x + 1) 2^-53 of itself:
-// 2^-23 of a turn at the far end, where (3 x + 1) e^-x is at most 1.6); its upper 32 bits, a signed number of half turns,
-// are rounded to fp32 (2^-25) and go to sincospif.  Integer arithmetic instead of fp64 products:
-// 75600 x 64 pairs took 74 us with those and take 14 (38.7 MB written, 6 us at the copy rate; the
-// rest is sincospif).  A thread keeps its pair and walks over the tokens.
+// the low 64 bits of the integer product.  turns_j comes from an fp64 quotient of the host's frequency e^-x,
+// which is within (3 x + 1) 2^-53 of itself; with the quotient's own rounding and that of 2 pi it is within
+// (3 x + 3) e^-x 2^-53 / (2 pi), at most 2^-54.  So the angle is within 2^-30 of a turn for |p| below 2^24 and
+// within 2^-23 for all; its upper 32 bits, a signed number of half turns, are rounded to fp32 (2^-25) and go
+// to sincospif.  Integer arithmetic instead of fp64 products: 75600 x 64 pairs took 74 us with those and
+// take 14 (38.7 MB written, 6 us at the copy rate); what bounds the rest has not been counted.  A
+// thread keeps its pair and walks over the tokens.
 __global__ void __launch_bounds__(256) rope_table_kernel(const int32_t* __restrict__ pos, int64_t T, int axes,
                                                          int pairs, float amplitude,
                                                          const __grid_constant__ RopeFreqs f,

@@ -582,6 +582,9 @@ fp4_status_t fp4_dequantize_heads(fp4_fmt_t fmt, const uint8_t* codes, const uin
  *            (device) [T_kv][H_kv][D] with k_stride, v_stride; o_bf16 (device, out) [T_q][H][D] with
  *            o_stride.  Strides are at least a token's elements and multiples of 8 (slices of
  *            a fused projection do).  D 64 or 128; H a multiple of H_kv, at most 128 times it.
+ *            Finite values of V that a row sees are below 2^88 in magnitude (sums of products with weights
+ *            that are not normalized yet are held in fp32); infinities and NaN outside the rows' ranges
+ *            cost time, in the tiles of 128 keys where ranges end.
  *            o may be q itself, and overlaps no key or value.
  *   scale    > 0 and below 1e30; softcap 0 (none) to 1e15 scale
  *   slopes   (device) fp32 [H] or NULL; q_pos: position of query row 0 on the keys' axis, below 2^40 in
