@@ -723,6 +723,13 @@ def _rows_like(out, what: str, x, dev: int, stream):
     return out, out.data_ptr(), x.shape[1] * x.shape[2]
 
 
+def _int64(value: int, what: str) -> int:
+    """value, which has to fit the C call's 64 bits: ctypes cuts what does not, and the call would see another number."""
+    if not -(1 << 63) <= value < 1 << 63:
+        raise ValueError(f"{what}: {value} does not fit 64 bits")
+    return value
+
+
 def _launch(dev: int, call, *args):
     """The call with CUDA device `dev` current (its stream is that device's current one)."""
     import torch
@@ -758,7 +765,7 @@ def rope_table(positions, axis_dims, theta: float = 10000.0, factor: float = 1.0
     pos = _expect(positions, "positions", torch.int32, dev)
     if table is None:
         table = _new(dev, stream, lambda: torch.empty((T, sum(axis_dims)), dtype=torch.float32, device=positions.device))
-    _launch(dev, fp4_rope_table, pos, T, len(axis_dims), axis_dims, theta, factor, window, amplitude,
+    _launch(dev, fp4_rope_table, pos, T, len(axis_dims), axis_dims, theta, factor, _int64(window, "window"), amplitude,
             _expect(table, "table", torch.float32, dev, (T, sum(axis_dims))), stream)
     return table
 
@@ -873,6 +880,7 @@ def linear_residual(x, pw: PackedWeight, residual=None, bias=None, act="none", g
     wsp, wgp = _expect(pw.sf, "weight scales", torch.uint8, dev), _expect(pw.w_global, "w_global", torch.float32, dev)
     if pw.sf.numel() != fp4_sf_bytes(pw.fmt, N, K):
         raise ValueError(f"weight scales: expected {fp4_sf_bytes(pw.fmt, N, K)} bytes, got {pw.sf.numel()}")
+    gate_rows = min(gate_rows, max(M, 1))
     gp = None if gate is None else _expect(gate, "gate", torch.float32, dev, (-(-M // gate_rows), N))
     if y is None:
         y = _new(dev, stream, lambda: torch.empty((M, N), dtype=torch.bfloat16, device=x.device))
@@ -895,6 +903,7 @@ def attn_ranges(q_offsets, k_offsets, T_q: int, T_kv: int, causal=False, prefix=
     qp = _expect(q_offsets, "q_offsets", torch.int32, dev, (docs + 1,))
     kp = _expect(k_offsets, "k_offsets", torch.int32, dev, (docs + 1,))
     pp = _expect(prefix, "prefix", torch.int32, dev, (docs,))
+    _int64(T_kv, "T_kv")
     start, end = (_new(dev, stream, lambda: q_offsets.new_empty(T_q)) for _ in range(2))
     _launch(dev, fp4_attn_ranges, qp, kp, docs, T_q, T_kv, causal, pp, start.data_ptr(), end.data_ptr(), stream)
     return start, end
@@ -925,7 +934,7 @@ def attn_bf16(q, k, v, scale: float, softcap: float = 0.0, slopes=None, q_pos: i
         workspace = _new(dev, stream, lambda: torch.empty(ws, dtype=torch.uint8, device=q.device))
     wp = _expect(workspace, "workspace", torch.uint8, dev)
     _launch(dev, fp4_attn_bf16, qp, q_stride, T_q, kp, k_stride, vp, v_stride, T_kv, H, H_kv, D, scale, softcap,
-            _expect(slopes, "slopes", torch.float32, dev, (H,)), q_pos,
+            _expect(slopes, "slopes", torch.float32, dev, (H,)), _int64(q_pos, "q_pos"),
             _expect(key_start, "key_start", torch.int32, dev, (T_q,)),
             _expect(key_end, "key_end", torch.int32, dev, (T_q,)), op, o_stride,
             None if lse is None else lse.data_ptr(), wp, 0 if workspace is None else workspace.numel(), stream)

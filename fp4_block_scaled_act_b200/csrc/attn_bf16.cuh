@@ -626,7 +626,7 @@ __global__ void __launch_bounds__(AB_THREADS, 1)
                             far = fmaxf(fmaxf(far, fabsf(__uint_as_float(v[q][y]))), fabsf(__uint_as_float(v[q][y + 1])));
                     // Each value takes the form of its own size.  The warp's vote, in which masked keys and other
                     // rows take part, only skips the other form where no value takes it: one form a tile by that
-                    // vote made the far one 1.3 times as fast, but a row's bits then hung on what it does not see.
+                    // vote made the far one 1.2 times as fast, but a row's bits then hung on what it does not see.
                     // (a NaN is passed over by the maximum and stays one in either form)
                     const uint64_t cc = f2_splat(p.c);
                     if (__all_sync(0xffffffffu, far * p.c <= 1.0f || tok < 0)) {
